@@ -13,6 +13,13 @@ Functions carry the C names:
     mega_moe_workspace_views(problem, workspace) -> dict of torch views into the workspace
     mega_moe_strerror(status) -> str
     mega_moe_abi_version() -> int
+
+and the operators in front of the layer, which make its inputs from a model's hidden state:
+
+    mega_moe_norm_quant(problem, x, weight, residual=None, residual_out=None, normed=None, q=None,
+                        q_sf=None, stream=None)
+    mega_moe_gate_logits(problem, x, weight, logits, stream=None)
+    mega_moe_gate_topk(problem, logits, topk_idx, topk_w, bias=None, num_valid=None, stream=None)
 """
 from __future__ import annotations
 
@@ -35,6 +42,12 @@ FLAG_WEIGHT_SF_KMAJOR = 16   # per-32 recipes: weight scales from mega_moe_trans
 FLAG_INTER_SF64 = 32         # FP8 recipe: intermediate float scales per 64 channels (L2 in two halves)
 FLAG_FUSED = 64              # the whole forward in one persistent cooperative launch
 FLAG_WEIGHT_E2M1_PAIRED = 128  # MXFP4: E2M1 weights in the row-pair layout of mega_moe_transform_weights
+
+DTYPE_BF16 = 0
+DTYPE_F32 = 1
+SCORE_SOFTMAX = 0
+SCORE_SIGMOID = 1
+FLAG_TOPK_RENORM = 1    # TopkProblem: divide the chosen scores by their sum
 
 ABI_VERSION = 1
 
@@ -61,6 +74,69 @@ class Problem(ctypes.Structure):
     @classmethod
     def make(cls, T, H, I, E, k, recipe=RECIPE_FP8_B128, swiglu_clamp=0.0, flags=0):
         return cls(int(T), int(H), int(I), int(E), int(k), int(recipe), float(swiglu_clamp), int(flags))
+
+
+class NormProblem(ctypes.Structure):
+    """mega_moe_norm_problem."""
+    _fields_ = [
+        ("num_tokens", ctypes.c_int64),
+        ("hidden", ctypes.c_int32),
+        ("recipe", ctypes.c_int32),
+        ("x_dtype", ctypes.c_int32),
+        ("weight_dtype", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+        ("flags", ctypes.c_uint32),
+        ("x_stride", ctypes.c_int64),
+        ("residual_stride", ctypes.c_int64),
+    ]
+
+    @classmethod
+    def make(cls, T, H, recipe=RECIPE_FP8_B128, x_dtype=DTYPE_BF16, weight_dtype=DTYPE_BF16, eps=1e-6, flags=0,
+             x_stride=0, residual_stride=0):
+        return cls(int(T), int(H), int(recipe), int(x_dtype), int(weight_dtype), float(eps), int(flags),
+                   int(x_stride), int(residual_stride))
+
+
+class GateProblem(ctypes.Structure):
+    """mega_moe_gate_problem."""
+    _fields_ = [
+        ("num_tokens", ctypes.c_int64),
+        ("hidden", ctypes.c_int32),
+        ("num_experts", ctypes.c_int32),
+        ("weight_dtype", ctypes.c_int32),
+        ("flags", ctypes.c_uint32),
+        ("x_stride", ctypes.c_int64),
+    ]
+
+    @classmethod
+    def make(cls, T, H, E, weight_dtype=DTYPE_BF16, flags=0, x_stride=0):
+        return cls(int(T), int(H), int(E), int(weight_dtype), int(flags), int(x_stride))
+
+
+class TopkProblem(ctypes.Structure):
+    """mega_moe_topk_problem."""
+    _fields_ = [
+        ("num_tokens", ctypes.c_int64),
+        ("num_experts", ctypes.c_int32),
+        ("topk", ctypes.c_int32),
+        ("score", ctypes.c_int32),
+        ("logits_dtype", ctypes.c_int32),
+        ("num_groups", ctypes.c_int32),
+        ("topk_groups", ctypes.c_int32),
+        ("group_top", ctypes.c_int32),
+        ("num_shared", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("shared_weight", ctypes.c_float),
+        ("flags", ctypes.c_uint32),
+        ("logits_stride", ctypes.c_int64),
+    ]
+
+    @classmethod
+    def make(cls, T, E, k, score=SCORE_SOFTMAX, logits_dtype=DTYPE_F32, num_groups=1, topk_groups=1, group_top=1,
+             num_shared=0, scale=1.0, shared_weight=1.0, flags=0, logits_stride=0):
+        return cls(int(T), int(E), int(k), int(score), int(logits_dtype), int(num_groups), int(topk_groups),
+                   int(group_top), int(num_shared), float(scale), float(shared_weight), int(flags),
+                   int(logits_stride))
 
 
 class _Views(ctypes.Structure):
@@ -108,6 +184,12 @@ def _load():
     lib.mega_moe_forward_noalloc.argtypes = [P, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
     lib.mega_moe_diag_mfma_block_sums.restype = ctypes.c_int
     lib.mega_moe_diag_mfma_block_sums.argtypes = [ctypes.c_int, vp, vp, vp, vp, vp, ctypes.c_int, vp]
+    lib.mega_moe_norm_quant.restype = ctypes.c_int
+    lib.mega_moe_norm_quant.argtypes = [ctypes.POINTER(NormProblem), vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.mega_moe_gate_logits.restype = ctypes.c_int
+    lib.mega_moe_gate_logits.argtypes = [ctypes.POINTER(GateProblem), vp, vp, vp, vp]
+    lib.mega_moe_gate_topk.restype = ctypes.c_int
+    lib.mega_moe_gate_topk.argtypes = [ctypes.POINTER(TopkProblem), vp, vp, vp, vp, vp, vp]
     if lib.mega_moe_abi_version() != ABI_VERSION:
         raise ImportError(f"{LIB_PATH} has ABI {lib.mega_moe_abi_version()}, expected {ABI_VERSION}")
     _lib = lib
@@ -361,6 +443,114 @@ def mega_moe_diag_mfma_block_sums(fmt: int, a, b, a_scale=None, b_scale=None, st
     if st:
         raise MegaMoEError(st, "mega_moe_diag_mfma_block_sums")
     return out
+
+
+def _dtype_of(code):
+    import torch
+    return {DTYPE_BF16: torch.bfloat16, DTYPE_F32: torch.float32}.get(code)
+
+
+def _check_rows(name, t, device, dtype, shape, stride):
+    """A [T, n] tensor whose rows are `stride` elements apart (0: n), as the problem says."""
+    if t.dtype != dtype or t.shape != shape or t.device != device:
+        raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}, expected {dtype} {shape} on {device}")
+    if shape[0] and shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    if shape[0] > 1 and t.stride(0) != (stride or shape[1]):
+        raise ValueError(f"the rows of {name} are {t.stride(0)} elements apart, the problem says {stride or shape[1]}")
+
+
+def _check_buffer(name, t, device, dtype, shape):
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}, expected {dtype} {shape}, contiguous, "
+                         f"on {device}")
+
+
+def _front_call(what, fn, problem, device, ptrs, stream):
+    """Call an operator in front of the layer with `device` current, on `stream` or its current stream."""
+    import torch
+    index = device.index
+    if stream is None:
+        handle = torch.cuda.current_stream(device).cuda_stream
+    else:
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if index == torch.cuda.current_device():
+        st = fn(ctypes.byref(problem), *ptrs, handle)
+    else:
+        with torch.cuda.device(index):
+            st = fn(ctypes.byref(problem), *ptrs, handle)
+    if st:
+        raise MegaMoEError(st, what)
+
+
+def mega_moe_norm_quant(problem: NormProblem, x, weight, residual=None, residual_out=None, normed=None, q=None,
+                        q_sf=None, stream=None) -> None:
+    """Residual addition, RMS norm and quantisation to the forward's 8-bit rows (include/mega_moe.h).
+    x, residual, residual_out: [T, H] of the problem's x_dtype with its row strides; weight [H];
+    outputs normed bf16 [T, H], q uint8 [T, H] with q_sf float32 [T, H/128] or uint8 [T, H/32], each
+    caller-allocated or None."""
+    import torch
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError("mega_moe_norm_quant needs device tensors")
+    T, H = problem.num_tokens, problem.hidden
+    xt, wt = _dtype_of(problem.x_dtype), _dtype_of(problem.weight_dtype)
+    _check_rows("x", x, dev, xt, (T, H), problem.x_stride)
+    _check_buffer("weight", weight, dev, wt, (H,))
+    if residual is not None:
+        _check_rows("residual", residual, dev, xt, (T, H), problem.residual_stride)
+    if residual_out is not None:
+        _check_rows("residual_out", residual_out, dev, xt, (T, H), problem.residual_stride)
+    if normed is not None:
+        _check_buffer("normed", normed, dev, torch.bfloat16, (T, H))
+    if q is not None:
+        _check_buffer("q", q, dev, torch.uint8, (T, H))
+    if q_sf is not None:
+        if problem.recipe == RECIPE_FP8_B128:
+            _check_buffer("q_sf", q_sf, dev, torch.float32, (T, H // 128))
+        else:
+            _check_buffer("q_sf", q_sf, dev, torch.uint8, (T, H // 32))
+    _front_call("mega_moe_norm_quant", _load().mega_moe_norm_quant, problem, dev,
+                [None if t is None else t.data_ptr() for t in (x, residual, weight, residual_out, normed, q, q_sf)],
+                stream)
+
+
+def mega_moe_gate_logits(problem: GateProblem, x, weight, logits, stream=None) -> None:
+    """logits[t, e] = sum_h x[t, h] weight[e, h]: x bf16 [T, H], weight [E, H] of the problem's
+    weight_dtype, logits float32 [T, E] (caller-allocated)."""
+    import torch
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError("mega_moe_gate_logits needs device tensors")
+    T, H, E = problem.num_tokens, problem.hidden, problem.num_experts
+    _check_rows("x", x, dev, torch.bfloat16, (T, H), problem.x_stride)
+    _check_buffer("weight", weight, dev, _dtype_of(problem.weight_dtype), (E, H))
+    _check_buffer("logits", logits, dev, torch.float32, (T, E))
+    _front_call("mega_moe_gate_logits", _load().mega_moe_gate_logits, problem, dev,
+                (x.data_ptr(), weight.data_ptr(), logits.data_ptr()), stream)
+
+
+def mega_moe_gate_topk(problem: TopkProblem, logits, topk_idx, topk_w, bias=None, num_valid=None,
+                       stream=None) -> None:
+    """Choice of experts from logits [T, E] (include/mega_moe.h): topk_idx int32 and topk_w float32
+    [T, topk + num_shared] (caller-allocated), bias float32 [E] or None, num_valid int32 [1] on the device
+    or None."""
+    import torch
+    dev = logits.device
+    if dev.type != "cuda":
+        raise ValueError("mega_moe_gate_topk needs device tensors")
+    T, E = problem.num_tokens, problem.num_experts
+    cols = problem.topk + problem.num_shared
+    _check_rows("logits", logits, dev, _dtype_of(problem.logits_dtype), (T, E), problem.logits_stride)
+    if bias is not None:
+        _check_buffer("bias", bias, dev, torch.float32, (E,))
+    if num_valid is not None:
+        _check_buffer("num_valid", num_valid, dev, torch.int32, (1,))
+    _check_buffer("topk_idx", topk_idx, dev, torch.int32, (T, cols))
+    _check_buffer("topk_w", topk_w, dev, torch.float32, (T, cols))
+    _front_call("mega_moe_gate_topk", _load().mega_moe_gate_topk, problem, dev,
+                (logits.data_ptr(), None if bias is None else bias.data_ptr(),
+                 None if num_valid is None else num_valid.data_ptr(), topk_idx.data_ptr(), topk_w.data_ptr()), stream)
 
 
 class MegaMoE:

@@ -11,6 +11,7 @@
 
 #include "mega_moe.h"
 #include "mm_common.h"
+#include "mm_front.h"
 
 #define MM_EXPORT extern "C" __attribute__((visibility("default")))
 
@@ -413,4 +414,178 @@ MM_EXPORT int mega_moe_diag_mfma_block_sums(int fmt, const void* a, const void* 
                            n_tiles, static_cast<hipStream_t>(stream)) != hipSuccess)
     return MEGA_MOE_ERR_HIP;
   return MEGA_MOE_OK;
+}
+
+// ----------------------------------------------------------- the operators in front of the layer
+namespace {
+
+// Byte ranges [lo, hi) of the buffers of one call.
+struct Range {
+  uintptr_t lo, hi;
+};
+
+inline Range range_of(const void* p, size_t bytes) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+  return {a, p ? a + bytes : a};
+}
+
+// Bytes from the first element of the first row to the last element of the last one.
+inline size_t rows_bytes(int64_t rows, int64_t stride, int64_t cols, size_t elem) {
+  return ((size_t)(rows - 1) * (size_t)stride + (size_t)cols) * elem;
+}
+
+inline bool overlap(const Range& a, const Range& b) { return a.lo < b.hi && b.lo < a.hi; }
+
+inline bool known_dtype(int d) { return d == MEGA_MOE_DTYPE_BF16 || d == MEGA_MOE_DTYPE_F32; }
+inline size_t dtype_bytes(int d) { return d == MEGA_MOE_DTYPE_BF16 ? 2 : 4; }
+
+constexpr int64_t kMaxStride = (int64_t)1 << 40;
+constexpr int64_t kMaxTokens = (int64_t)1 << 30;
+
+inline bool bad_stride(int64_t stride, int64_t cols, int64_t step) {
+  return stride != 0 && (stride < cols || stride % step || stride >= kMaxStride);
+}
+
+inline bool bad_hidden(int h) { return h <= 0 || h % 128 || h > 16384; }
+
+}  // namespace
+
+MM_EXPORT int mega_moe_norm_quant(const mega_moe_norm_problem* p, const void* x, const void* residual,
+                                  const void* weight, void* residual_out, void* normed, void* q, void* q_sf,
+                                  void* stream) {
+  if (!p) return MEGA_MOE_ERR_NULL_POINTER;
+  if (p->num_tokens < 0 || p->num_tokens >= kMaxTokens || bad_hidden(p->hidden) || p->flags)
+    return MEGA_MOE_ERR_INVALID_ARG;
+  if (p->recipe != MEGA_MOE_RECIPE_FP8_B128 && p->recipe != MEGA_MOE_RECIPE_MXFP4W_B32 &&
+      p->recipe != MEGA_MOE_RECIPE_MXFP8_B32)
+    return MEGA_MOE_ERR_INVALID_ARG;
+  if (!known_dtype(p->x_dtype) || !known_dtype(p->weight_dtype)) return MEGA_MOE_ERR_INVALID_ARG;
+  if (!(p->eps > 0.f) || std::isinf(p->eps)) return MEGA_MOE_ERR_INVALID_ARG;
+  const int64_t T = p->num_tokens, H = p->hidden;
+  const size_t xb = dtype_bytes(p->x_dtype);
+  if (bad_stride(p->x_stride, H, 16 / (int64_t)xb) || bad_stride(p->residual_stride, H, 16 / (int64_t)xb))
+    return MEGA_MOE_ERR_INVALID_ARG;
+  if (T == 0) return MEGA_MOE_OK;
+  if (!x || !weight || (!q) != (!q_sf)) return MEGA_MOE_ERR_NULL_POINTER;
+  if (!normed && !q) return MEGA_MOE_ERR_INVALID_ARG;
+  const void* ptrs[] = {x, residual, weight, residual_out, normed, q, q_sf};
+  for (const void* ptr : ptrs)
+    if (misaligned(ptr)) return MEGA_MOE_ERR_MISALIGNED;
+  const int64_t xs = p->x_stride ? p->x_stride : H, rs = p->residual_stride ? p->residual_stride : H;
+  const size_t sf_bytes = (size_t)T * (p->recipe == MEGA_MOE_RECIPE_FP8_B128 ? H / 128 * 4 : H / 32);
+  const Range in[] = {range_of(x, rows_bytes(T, xs, H, xb)), range_of(residual, rows_bytes(T, rs, H, xb)),
+                      range_of(weight, H * dtype_bytes(p->weight_dtype))};
+  const Range out[] = {range_of(residual_out, rows_bytes(T, rs, H, xb)), range_of(normed, (size_t)T * H * 2),
+                       range_of(q, (size_t)T * H), range_of(q_sf, sf_bytes)};
+  for (int o = 0; o < 4; ++o) {
+    for (int i = 0; i < 3; ++i) {
+      // in place: each thread has read its own elements of the row before it writes them
+      if (o == 0 && ((i == 1 && residual_out == residual) || (i == 0 && residual_out == x && xs == rs))) continue;
+      if (overlap(out[o], in[i])) return MEGA_MOE_ERR_INVALID_ARG;
+    }
+    for (int k = o + 1; k < 4; ++k)
+      if (overlap(out[o], out[k])) return MEGA_MOE_ERR_INVALID_ARG;
+  }
+  const int st = check_device();
+  if (st) return st;
+  mm::NormArgs a{};
+  a.x = x;
+  a.residual = residual;
+  a.weight = weight;
+  a.residual_out = residual_out;
+  a.normed = static_cast<uint16_t*>(normed);
+  a.q = static_cast<uint8_t*>(q);
+  a.q_sf = q_sf;
+  a.x_stride = xs;
+  a.residual_stride = rs;
+  a.T = (int)T;
+  a.H = (int)H;
+  a.eps = p->eps;
+  a.x_f32 = p->x_dtype == MEGA_MOE_DTYPE_F32;
+  a.w_f32 = p->weight_dtype == MEGA_MOE_DTYPE_F32;
+  a.per32 = p->recipe != MEGA_MOE_RECIPE_FP8_B128;
+  return mm::launch_norm_quant(a, static_cast<hipStream_t>(stream)) == hipSuccess ? MEGA_MOE_OK : MEGA_MOE_ERR_HIP;
+}
+
+MM_EXPORT int mega_moe_gate_logits(const mega_moe_gate_problem* p, const void* x, const void* w, float* logits,
+                                   void* stream) {
+  if (!p) return MEGA_MOE_ERR_NULL_POINTER;
+  if (p->num_tokens < 0 || p->num_tokens >= kMaxTokens || bad_hidden(p->hidden) || p->flags)
+    return MEGA_MOE_ERR_INVALID_ARG;
+  if (p->num_experts < 1 || p->num_experts > mm::kMaxExperts || !known_dtype(p->weight_dtype) ||
+      bad_stride(p->x_stride, p->hidden, 8))
+    return MEGA_MOE_ERR_INVALID_ARG;
+  const int64_t T = p->num_tokens, H = p->hidden, E = p->num_experts;
+  if (T == 0) return MEGA_MOE_OK;
+  if (!x || !w || !logits) return MEGA_MOE_ERR_NULL_POINTER;
+  if (misaligned(x) || misaligned(w) || misaligned(logits)) return MEGA_MOE_ERR_MISALIGNED;
+  const int64_t xs = p->x_stride ? p->x_stride : H;
+  const Range out = range_of(logits, (size_t)T * E * 4);
+  if (overlap(out, range_of(x, rows_bytes(T, xs, H, 2))) ||
+      overlap(out, range_of(w, (size_t)E * H * dtype_bytes(p->weight_dtype))))
+    return MEGA_MOE_ERR_INVALID_ARG;
+  const int st = check_device();
+  if (st) return st;
+  mm::GateArgs a{};
+  a.x = static_cast<const uint16_t*>(x);
+  a.w = w;
+  a.logits = logits;
+  a.x_stride = xs;
+  a.T = (int)T;
+  a.H = (int)H;
+  a.E = (int)E;
+  a.w_f32 = p->weight_dtype == MEGA_MOE_DTYPE_F32;
+  return mm::launch_gate_logits(a, static_cast<hipStream_t>(stream)) == hipSuccess ? MEGA_MOE_OK : MEGA_MOE_ERR_HIP;
+}
+
+MM_EXPORT int mega_moe_gate_topk(const mega_moe_topk_problem* p, const void* logits, const float* bias,
+                                 const int32_t* num_valid, int32_t* topk_idx, float* topk_w, void* stream) {
+  if (!p) return MEGA_MOE_ERR_NULL_POINTER;
+  const int64_t T = p->num_tokens, E = p->num_experts, k = p->topk, S = p->num_shared;
+  if (T < 0 || E < 1 || S < 0 || E + S > mm::kMaxExperts || k < 1 || k + S > mm::kMaxTopk)
+    return MEGA_MOE_ERR_INVALID_ARG;
+  if (T >= kMaxTokens || T * (k + S) >= kMaxTokens) return MEGA_MOE_ERR_INVALID_ARG;
+  if (p->score != MEGA_MOE_SCORE_SOFTMAX && p->score != MEGA_MOE_SCORE_SIGMOID) return MEGA_MOE_ERR_INVALID_ARG;
+  if (!known_dtype(p->logits_dtype) || (p->flags & ~MEGA_MOE_FLAG_TOPK_RENORM)) return MEGA_MOE_ERR_INVALID_ARG;
+  const int64_t G = p->num_groups, KG = p->topk_groups;
+  if (G < 1 || G > mm::kMaxGroups || E % G || KG < 1 || KG > G || p->group_top < 1 || p->group_top > 2 ||
+      k > E / G * KG)
+    return MEGA_MOE_ERR_INVALID_ARG;
+  if (!std::isfinite(p->scale) || !std::isfinite(p->shared_weight)) return MEGA_MOE_ERR_INVALID_ARG;
+  if (bad_stride(p->logits_stride, E, 1)) return MEGA_MOE_ERR_INVALID_ARG;
+  if (T == 0) return MEGA_MOE_OK;
+  if (!logits || !topk_idx || !topk_w) return MEGA_MOE_ERR_NULL_POINTER;
+  if (misaligned(logits) || misaligned(bias) || misaligned(topk_idx) || misaligned(topk_w) ||
+      (reinterpret_cast<uintptr_t>(num_valid) & 3u))
+    return MEGA_MOE_ERR_MISALIGNED;
+  const int64_t ls = p->logits_stride ? p->logits_stride : E;
+  const size_t ob = (size_t)T * (k + S) * 4;
+  const Range in[] = {range_of(logits, rows_bytes(T, ls, E, dtype_bytes(p->logits_dtype))), range_of(bias, E * 4),
+                      range_of(num_valid, 4)};
+  const Range oi = range_of(topk_idx, ob), ow = range_of(topk_w, ob);
+  if (overlap(oi, ow)) return MEGA_MOE_ERR_INVALID_ARG;
+  for (const Range& r : in)
+    if (overlap(oi, r) || overlap(ow, r)) return MEGA_MOE_ERR_INVALID_ARG;
+  const int st = check_device();
+  if (st) return st;
+  mm::TopkArgs a{};
+  a.logits = logits;
+  a.bias = bias;
+  a.num_valid = num_valid;
+  a.idx = topk_idx;
+  a.w = topk_w;
+  a.stride = ls;
+  a.T = (int)T;
+  a.E = (int)E;
+  a.k = (int)k;
+  a.S = (int)S;
+  a.G = (int)G;
+  a.KG = (int)KG;
+  a.group_top = p->group_top;
+  a.sigmoid = p->score == MEGA_MOE_SCORE_SIGMOID;
+  a.renorm = (p->flags & MEGA_MOE_FLAG_TOPK_RENORM) != 0;
+  a.bf16 = p->logits_dtype == MEGA_MOE_DTYPE_BF16;
+  a.scale = p->scale;
+  a.shared_weight = p->shared_weight;
+  return mm::launch_gate_topk(a, static_cast<hipStream_t>(stream)) == hipSuccess ? MEGA_MOE_OK : MEGA_MOE_ERR_HIP;
 }

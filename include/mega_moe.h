@@ -290,6 +290,122 @@ int mega_moe_workspace_views(const mega_moe_problem* p, const void* workspace,
 int mega_moe_diag_mfma_block_sums(int fmt, const void* a, const void* b, const void* a_scale,
                                   const void* b_scale, float* out, int n_tiles, void* stream);
 
+/* ------------------------------------------------------------------------------------------
+ * The operators in front of the layer: what turns a model's hidden state into the inputs of
+ * mega_moe_forward.  In the order of their use:
+ *
+ *   mega_moe_norm_quant    residual addition, RMS norm, 8-bit rows with the recipe's scales
+ *                          (x and x_sf of the forward) and the BF16 rows the gate reads
+ *   mega_moe_gate_logits   logits[t, e] = sum_h x[t, h] * w[e, h]
+ *   mega_moe_gate_topk     scores, balance bias, expert groups, top-k, weights (topk_idx and
+ *                          topk_w of the forward), always-on shared experts appended
+ *
+ * They need no workspace, allocate and synchronise nothing, keep nothing between calls and can be
+ * captured into a HIP graph; each is one kernel launch on `stream` (a hipStream_t, NULL for the
+ * default stream), whose device has to be the current one.  Pointers are device memory, 16-byte
+ * aligned unless stated.  Arguments are validated synchronously, before the device is touched;
+ * num_tokens == 0 is a valid no-op.  An output overlaps no input and no other output, from its
+ * first element to its last, except where stated (INVALID_ARG).  Results are repeatable bit for bit.  Errors: INVALID_ARG, NULL_POINTER,
+ * MISALIGNED, UNSUPPORTED_DEVICE, HIP. */
+typedef enum { MEGA_MOE_DTYPE_BF16 = 0, MEGA_MOE_DTYPE_F32 = 1 } mega_moe_dtype;
+typedef enum { MEGA_MOE_SCORE_SOFTMAX = 0, MEGA_MOE_SCORE_SIGMOID = 1 } mega_moe_score;
+
+typedef struct {
+  int64_t num_tokens;      /* T in [0, 2^30) */
+  int32_t hidden;          /* H in (0, 16384], multiple of 128 */
+  int32_t recipe;          /* mega_moe_recipe: which scales q_sf holds */
+  int32_t x_dtype;         /* mega_moe_dtype of x, residual and residual_out */
+  int32_t weight_dtype;    /* mega_moe_dtype of weight */
+  float eps;               /* finite, > 0 */
+  uint32_t flags;          /* 0 */
+  int64_t x_stride;        /* elements from one row of x to the next: 0 (= H), or >= H in whole
+                              16-byte steps (a multiple of 8 for BF16, of 4 for F32), < 2^40 */
+  int64_t residual_stride; /* the same for residual and residual_out */
+} mega_moe_norm_problem;
+
+/* Residual addition, RMS norm and quantisation of each row:
+ *   h = x + residual              (float32; x alone where residual is NULL)
+ *   residual_out = h              (rounded to x_dtype)
+ *   v = h / sqrt(mean(h^2) + eps) * weight          (from the unrounded h; the mean in float64)
+ *   normed = bf16(v)
+ *   q, q_sf = v in 8 bits as the forward's x, x_sf of the recipe: per group of 128 columns
+ *     q_sf = amax/448 (float32), q = E4M3(v / q_sf); or per group of 32 the UE8M0 code of the
+ *     smallest power of two s with amax/s <= 448 (at least 2^-127; decided as if in float64), and
+ *     q = E4M3(v / s).  An all-zero group has scale 0 (code 0) and codes 0.
+ * A row with a value that is not finite (in h) has NaN normed, q and q_sf (E4M3 0x7F or 0xFF, UE8M0
+ * code 255), a group with a v that is not finite has NaN q and q_sf; other rows and groups are
+ * not affected.
+ *   x            [T, H] x_dtype, rows x_stride apart
+ *   residual     [T, H] x_dtype, rows residual_stride apart, or NULL
+ *   weight       [H] weight_dtype
+ *   residual_out [T, H] x_dtype, rows residual_stride apart, or NULL; may be the residual itself
+ *                (in place), or x where both strides are the same
+ *   normed       bf16 [T, H], or NULL
+ *   q            u8 [T, H], q_sf f32 [T, H/128] | u8 [T, H/32] (per-32 recipes): both or neither
+ * normed, or q and q_sf, must be given (INVALID_ARG otherwise). */
+int mega_moe_norm_quant(const mega_moe_norm_problem* p, const void* x, const void* residual,
+                        const void* weight, void* residual_out, void* normed, void* q, void* q_sf,
+                        void* stream);
+
+typedef struct {
+  int64_t num_tokens;    /* T in [0, 2^30) */
+  int32_t hidden;        /* H in (0, 16384], multiple of 128 */
+  int32_t num_experts;   /* E in [1, 8192] */
+  int32_t weight_dtype;  /* mega_moe_dtype of w */
+  uint32_t flags;        /* 0 */
+  int64_t x_stride;      /* elements from one row of x to the next: 0 (= H), or >= H and a multiple
+                            of 8, < 2^40 */
+} mega_moe_gate_problem;
+
+/* Gate product: logits[t, e] = sum_h x[t, h] * w[e, h], products exact, sums in float32.
+ *   x bf16 [T, H], rows x_stride apart;  w [E, H] weight_dtype;  logits f32 [T, E]
+ * Float32 weights are multiplied as the sum of three BF16 terms, which hold every float32 of
+ * magnitude 2^-110 or more exactly; with them an infinity in x or w gives NaN.  A value that is not
+ * finite affects only the logits of its row of x or of its expert. */
+int mega_moe_gate_logits(const mega_moe_gate_problem* p, const void* x, const void* w, float* logits,
+                         void* stream);
+
+/* flags of mega_moe_topk_problem: divide the chosen experts' scores by their sum + 1e-20. */
+#define MEGA_MOE_FLAG_TOPK_RENORM 1u
+
+typedef struct {
+  int64_t num_tokens;     /* T >= 0, T * (topk + num_shared) below 2^30 */
+  int32_t num_experts;    /* E routed experts, E >= 1, E + num_shared <= 8192 */
+  int32_t topk;           /* k >= 1 experts a token, k + num_shared <= 64,
+                             k <= topk_groups * E / num_groups */
+  int32_t score;          /* mega_moe_score */
+  int32_t logits_dtype;   /* mega_moe_dtype of logits */
+  int32_t num_groups;     /* groups of E / num_groups consecutive experts, in [1, 64], divides E */
+  int32_t topk_groups;    /* groups kept a token, in [1, num_groups] */
+  int32_t group_top;      /* a group's value: 1: its best expert's, 2: the sum of its two best */
+  int32_t num_shared;     /* S >= 0 always-on experts, ids E .. E + S - 1, in the last S columns */
+  float scale;            /* finite; the routed experts' weights are multiplied by it */
+  float shared_weight;    /* finite; the shared experts' weight */
+  uint32_t flags;         /* MEGA_MOE_FLAG_TOPK_* */
+  int64_t logits_stride;  /* elements from one row of logits to the next: 0 (= E), or >= E, < 2^40 */
+} mega_moe_topk_problem;
+
+/* Choice of experts.  For each row of logits l:
+ *   s_e = softmax(l)_e or sigmoid(l_e);  c_e = s_e + bias_e, or s_e where bias is NULL
+ *   a group's value is the largest c_e in it, or the sum of its two largest (of one where it has no
+ *   second candidate); the topk_groups best groups are kept
+ *   the k experts with the largest c_e in these groups, in descending order, go to topk_idx[t, 0..k)
+ *   w_e = s_e (without the bias), divided by the sum over the chosen + 1e-20 with
+ *   MEGA_MOE_FLAG_TOPK_RENORM, times scale, go to topk_w
+ * Order is decided as if c were computed in float64, without a bias in the order of l itself; of
+ * equal ones the lowest id (group) comes first.  A logit that is NaN or -inf counts in no softmax and its
+ * expert is never chosen; nor is one whose bias is NaN or -inf.  Experts with a logit of +inf share
+ * the whole softmax.  Where there are fewer than k experts to choose, the columns left have id -1
+ * and weight 0.
+ *   logits     [T, E] logits_dtype, rows logits_stride apart
+ *   bias       f32 [E] or NULL
+ *   topk_idx   i32 [T, k + S], topk_w f32 [T, k + S]
+ *   num_valid  i32 [1] in device memory (4-byte aligned) or NULL: rows from *num_valid on (the padding
+ *              of a captured batch) get ids -1 and weights 0, the shared columns too; their logits are
+ *              not looked at */
+int mega_moe_gate_topk(const mega_moe_topk_problem* p, const void* logits, const float* bias,
+                       const int32_t* num_valid, int32_t* topk_idx, float* topk_w, void* stream);
+
 /* Static text for a status code. */
 const char* mega_moe_strerror(int status);
 
