@@ -513,7 +513,7 @@ MM_EXPORT int mega_moe_gate_logits(const mega_moe_gate_problem* p, const void* x
   if (p->num_tokens < 0 || p->num_tokens >= kMaxTokens || bad_hidden(p->hidden) || p->flags)
     return MEGA_MOE_ERR_INVALID_ARG;
   if (p->num_experts < 1 || p->num_experts > mm::kMaxExperts || !known_dtype(p->weight_dtype) ||
-      bad_stride(p->x_stride, p->hidden, 8))
+      bad_stride(p->x_stride, p->hidden, 8) || p->x_stride > mm::kMaxGateStride)
     return MEGA_MOE_ERR_INVALID_ARG;
   const int64_t T = p->num_tokens, H = p->hidden, E = p->num_experts;
   if (T == 0) return MEGA_MOE_OK;

@@ -7,6 +7,7 @@
 namespace mm {
 
 constexpr int kMaxGroups = 64;        // expert groups: one lane of a wave each
+constexpr long kMaxGateStride = 1 << 22;  // the gate addresses a tile's rows of x with 31-bit offsets
 
 struct NormArgs {
   const void* x;             // [T, H] bf16 | f32, rows x_stride apart

@@ -1,9 +1,9 @@
 // Gate product: logits[t, e] = sum_h x[t, h] w[e, h] with BF16 MFMA, float32 sums.
 //
 // Weights are the MFMA's A operand (rows are experts) and tokens its B operand (columns), so a lane
-// ends with four consecutive experts of one token and stores them as one float4.  Float32 weights
-// are split into three BF16 terms of 8 significant bits each (w = hi + mid + lo exactly, by
-// truncation) and multiplied by three MFMAs into the same sum.
+// ends with four consecutive experts of one token.  Float32 weights are split into three BF16 terms of
+// 8 significant bits each (w = hi + mid + lo exactly, by truncation) and multiplied by three MFMAs
+// into the same sum.
 #include "mm_front.h"
 
 namespace mm {
@@ -11,79 +11,300 @@ namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-__device__ __forceinline__ v4f mfma_bf16(const uint4& a, const uint4& b, v4f c) {
+__device__ __forceinline__ v4f mfma_bf16(const v4i& a, const v4i& b, v4f c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
 // The upper halves of two words: two BF16 by truncation.
-__device__ __forceinline__ uint32_t upper_halves(float lo, float hi) {
-  return __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
+__device__ __forceinline__ int upper_halves(int lo, int hi) {
+  return (int)__builtin_amdgcn_perm((uint32_t)hi, (uint32_t)lo, 0x07060302u);
 }
-__device__ __forceinline__ float truncated(float v) { return __uint_as_float(__float_as_uint(v) & 0xFFFF0000u); }
 
-// Eight float32 values as three BF16 operands whose sum they are.
-__device__ __forceinline__ void split3(const float (&v)[8], uint4 (&t)[3]) {
-  float r[8];
+// What is left of a float32 once its upper half is taken off, exactly.
+__device__ __forceinline__ int lower_part(int v) {
+  return __builtin_bit_cast(int, __builtin_bit_cast(float, v) - __builtin_bit_cast(float, v & (int)0xFFFF0000));
+}
+
+// acc += w x for 8 float32 weights a lane (lo, hi) as three BF16 operands whose sum they are.
+__device__ __forceinline__ v4f mfma_split(v4i lo, v4i hi, const v4i& b, v4f acc) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) r[i] = v[i];
+  for (int term = 0; term < 3; ++term) {
+    const v4i t = {upper_halves(lo[0], lo[1]), upper_halves(lo[2], lo[3]), upper_halves(hi[0], hi[1]),
+                   upper_halves(hi[2], hi[3])};
+    acc = mfma_bf16(t, b, acc);
+    if (term == 2) break;
 #pragma unroll
-  for (int p = 0; p < 3; ++p) {
-    t[p] = make_uint4(upper_halves(r[0], r[1]), upper_halves(r[2], r[3]), upper_halves(r[4], r[5]), upper_halves(r[6], r[7]));
+    for (int i = 0; i < 4; ++i) {
+      lo[i] = lower_part(lo[i]);
+      hi[i] = lower_part(hi[i]);
+    }
+  }
+  return acc;
+}
+
+// A 16-byte load of each lane from a buffer into consecutive LDS bytes from the wave-uniform `lds` on.
+// Offsets at or past the buffer's size read zeros.
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+__device__ __forceinline__ rsrc_t make_rsrc(const void* base, size_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)(uint32_t)bytes, 0x00020000);
+}
+__device__ __forceinline__ void lds_load16(rsrc_t r, uint32_t voff, uint32_t soff, void* lds) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, voff, (int)soff, 0, 0);
+}
+template <int kN>
+__device__ __forceinline__ void wait_vmcnt() {
+  __builtin_amdgcn_s_waitcnt((kN & 0xF) | ((kN >> 4) << 14) | (0x7 << 4) | (0xF << 8));
+}
+
+// One workgroup per tile of 16 kM experts x 16 kN tokens.  Its kW waves share K: wave w takes the
+// steps of 64 columns w, w + kW, ..., each for the whole tile, through a ring of its own in LDS (kSW
+// steps of weights, kSX of tokens), so the loop has no barrier; the waves' sums meet in LDS at the end.
+// A step's weights are taken in kP parts: while one part is multiplied the next one is read into
+// registers, and its place in the ring is filled again at once.
+//
+// Rows are fetched as whole 128-byte lines (8 rows x 128 bytes a load): operands loaded straight into
+// registers touch 64 bytes of 16 rows, and the L2 delivers lines, half of each for nothing.
+// In LDS a row's eight 16-byte chunks are permuted by (row / 2) % 8, so that the 16 rows of an
+// operand read fall into different banks.
+template <bool kWF32, int kM, int kN, int kW, int kSW, int kSX, int kP>
+__global__ __launch_bounds__(64 * kW) void k_gate(GateArgs a, int etiles, long tiles) {
+  constexpr int kWB = kWF32 ? 4 : 2;                     // bytes a weight
+  constexpr int kHalves = kWF32 ? 2 : 1;                 // 128-byte lines of a weight row in a step
+  constexpr int kMP = kM / kP;                           // operands of 16 experts in a part
+  constexpr int kLX = 2 * kN, kLP = 2 * kMP * kHalves, kLW = kP * kLP;   // loads of a step / part
+  // Loads issued since a part's own when it is waited for (a step's tokens go out with its part 0):
+  // the rest of that step, the steps between, and what the present step has issued before this part.
+  static_assert(kSX >= kSW && kM % kP == 0 && (kP == 1 || kP % 2 == 0), "");
+  constexpr int kLater0 = kLW - kLP + (kSW - 1) * (kLX + kLW), kLater = kLater0 + kLX;
+  static_assert(kLater < 64, "vmcnt holds 6 bits");
+  constexpr int kXBytes = kLX * 1024, kWBytes = kLW * 1024;
+  constexpr int kRing = kSX * kXBytes + kSW * kWBytes;   // a wave's LDS
+  constexpr int kSums = kM * kN * 1024;                  // a wave's sums
+  __shared__ __align__(1024) char lds[kW * (kRing > kSums ? kRing : kSums)];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 15, lg = lane >> 4;
+  const int per = gridDim.x >> 3;
+  const long tile = (long)(blockIdx.x & 7) * per + (blockIdx.x >> 3);   // each XCD walks neighbouring tiles
+  if (tile >= tiles) return;
+  const int e0 = (int)(tile % etiles) * 16 * kM;
+  const long t0 = tile / etiles * 16 * kN;
+  char* ring = lds + wave * kRing;
+
+  // buffers of this tile's rows (at most 2^30 bytes): rows past the last one are out of range and read
+  // zeros, or repeat the first ones; neither is stored
+  const int erows = min(16 * kM, a.E - e0), trows = (int)min((long)(16 * kN), a.T - t0);
+  const uint32_t wstride = (uint32_t)a.H * kWB, xstride = (uint32_t)(a.x_stride * 2);
+  const rsrc_t wr = make_rsrc(static_cast<const char*>(a.w) + (size_t)e0 * wstride, (size_t)erows * wstride);
+  const rsrc_t xr = make_rsrc(a.x + (size_t)t0 * a.x_stride, (size_t)(trows - 1) * xstride + (size_t)a.H * 2);
+  // lane l of a load: row l / 8 of its eight, chunk l % 8 of the line in LDS, which holds the line's
+  // chunk (l % 8) ^ (row / 2 % 8); rows 8 .. 15 of an operand are the odd loads
+  const int sub = lane >> 3;
+  uint32_t wlane[2], xlane[2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] -= truncated(r[i]);
+  for (int o = 0; o < 2; ++o) {
+    const uint32_t chunk = 16u * (uint32_t)((lane & 7) ^ (4 * o + (sub >> 1)));
+    wlane[o] = (uint32_t)sub * wstride + chunk;
+    xlane[o] = (uint32_t)sub * xstride + chunk;
+  }
+  // operand reads: row col, chunk c of its line
+  const auto chunk_at = [&](int c) { return col * 128 + ((c ^ (col >> 1)) * 16); };
+
+  const int all = a.H / 64, steps = all > wave ? (all - wave + kW - 1) / kW : 0;
+  // Out of range is what lies at or past the buffer's size less the scalar offset, so the scalar offset
+  // itself stays inside: loads of a step past the last one, which count but fetch nothing, get a lane
+  // offset of 2^31 and scalar offset 0, and loads of eight rows that are all past the tile's last
+  // take the first eight.
+  const auto beyond = [&](int i) { return i < steps ? 0u : 0x80000000u; };
+  const auto column = [&](int i) { return i < steps ? (uint32_t)(wave + kW * i) : 0u; };
+  const auto rows_at = [&](int r, int rows, uint32_t stride) { return r < rows ? (uint32_t)r * stride : 0u; };
+  const auto fetch_w = [&](int i, int slot, int p) {
+    const uint32_t k = column(i) * (128 * kHalves), out = beyond(i);
+    char* to = ring + kSX * kXBytes + slot * kWBytes + p * kLP * 1024;
+#pragma unroll
+    for (int m = 0; m < 2 * kMP; ++m)
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h)
+        lds_load16(wr, wlane[m & 1] + out, k + 128 * h + rows_at(8 * (2 * kMP * p + m), erows, wstride),
+                   to + (h * 2 * kMP + m) * 1024);
+  };
+  const auto fetch_x = [&](int i, int slot) {
+    const uint32_t k = column(i) * 128, out = beyond(i);
+    char* to = ring + slot * kXBytes;
+#pragma unroll
+    for (int n = 0; n < 2 * kN; ++n) lds_load16(xr, xlane[n & 1] + out, k + rows_at(8 * n, trows, xstride), to + n * 1024);
+  };
+
+  v4i X[2][2][kN], W[2][2][kMP][kHalves];
+  const auto read_x = [&](int slot, v4i (&to)[2][kN]) {
+    const char* xs = ring + slot * kXBytes;
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int n = 0; n < kN; ++n) to[s][n] = *reinterpret_cast<const v4i*>(xs + n * 2048 + chunk_at(4 * s + lg));
+  };
+  const auto read_w = [&](int slot, int p, v4i (&to)[2][kMP][kHalves]) {
+    const char* ws = ring + kSX * kXBytes + slot * kWBytes + p * kLP * 1024;
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int m = 0; m < kMP; ++m) {
+        if constexpr (kWF32) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            to[s][m][h] = *reinterpret_cast<const v4i*>(ws + (s * 2 * kMP + 2 * m) * 1024 + chunk_at(2 * lg + h));
+        } else {
+          to[s][m][0] = *reinterpret_cast<const v4i*>(ws + m * 2048 + chunk_at(4 * s + lg));
+        }
+      }
+  };
+
+  v4f acc[kM][kN];
+#pragma unroll
+  for (int m = 0; m < kM; ++m)
+#pragma unroll
+    for (int n = 0; n < kN; ++n) acc[m][n] = v4f{0.f, 0.f, 0.f, 0.f};
+
+  if (steps > 0) {
+#pragma unroll
+    for (int j = -kSX; j < 0; ++j) {
+      fetch_x(j + kSX, j + kSX);
+      if (j + kSW >= 0)
+#pragma unroll
+        for (int p = 0; p < kP; ++p) fetch_w(j + kSW, j + kSW, p);
+    }
+    int sw = 0, sx = 0;                            // the ring's slots of step i
+    wait_vmcnt<kLater0>();
+    asm volatile("" ::: "memory");
+    read_x(0, X[0]);
+    read_w(0, 0, W[0]);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    fetch_x(kSX, 0);
+    fetch_w(kSW, 0, 0);
+    for (int i0 = 0; i0 < steps; i0 += 2) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int i = i0 + u;
+        if (u == 1 && i >= steps) break;
+        const int sx1 = sx + 1 == kSX ? 0 : sx + 1, sw1 = sw + 1 == kSW ? 0 : sw + 1;
+#pragma unroll
+        for (int p = 0; p < kP; ++p) {
+          const int b = (u * kP + p) & 1;          // registers of this part
+          if (p + 1 < kP) {
+            wait_vmcnt<kLater>();
+            asm volatile("" ::: "memory");
+            read_w(sw, p + 1, W[b ^ 1]);
+          } else {
+            wait_vmcnt<kLater0>();
+            asm volatile("" ::: "memory");
+            read_x(sx1, X[u ^ 1]);
+            read_w(sw1, 0, W[b ^ 1]);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int m = 0; m < kMP; ++m)
+#pragma unroll
+              for (int n = 0; n < kN; ++n) {
+                v4f& c = acc[p * kMP + m][n];
+                if constexpr (kWF32) c = mfma_split(W[b][s][m][0], W[b][s][m][1], X[u][s][n], c);
+                else c = mfma_bf16(W[b][s][m][0], X[u][s][n], c);
+              }
+          __builtin_amdgcn_sched_barrier(0);
+          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // read: the place may be filled again
+          if (p + 1 < kP) {
+            fetch_w(i + kSW, sw, p + 1);
+          } else {
+            fetch_x(i + 1 + kSX, sx1);
+            fetch_w(i + 1 + kSW, sw1, 0);
+          }
+        }
+        sx = sx1;
+        sw = sw1;
+      }
+    }
+  }
+
+  wait_vmcnt<0>();                                 // this wave's loads into LDS have landed
+  __syncthreads();                                 // and every other's: the rings become the sums
+  v4f* sums = reinterpret_cast<v4f*>(lds);
+#pragma unroll
+  for (int m = 0; m < kM; ++m)
+#pragma unroll
+    for (int n = 0; n < kN; ++n) sums[(wave * kM * kN + m * kN + n) * 64 + lane] = acc[m][n];
+  __syncthreads();
+  for (int j = wave; j < kM * kN; j += kW) {
+    v4f sum = sums[j * 64 + lane];
+#pragma unroll
+    for (int w = 1; w < kW; ++w) sum += sums[(w * kM * kN + j) * 64 + lane];
+    const int e = e0 + 16 * (j / kN) + 4 * lg;
+    const long t = t0 + 16 * (j % kN) + col;
+    if (t >= a.T) continue;
+    float* out = a.logits + (size_t)t * a.E + e;
+    if ((a.E & 3) == 0) {
+      if (e < a.E) *reinterpret_cast<v4f*>(out) = sum;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (e + i < a.E) out[i] = sum[i];
+    }
   }
 }
 
-// One workgroup per tile of 16 experts x 16 tokens, four waves sharing K, joined through LDS.
-template <bool kWF32>
-__global__ __launch_bounds__(256) void k_gate(GateArgs a) {
-  __shared__ v4f s_part[4][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, lg = lane >> 4;
-  const int et = (a.E + 15) / 16;
-  const long tiles = (long)et * ((a.T + 15) / 16);
-  for (long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const int e0 = (int)(tile % et) * 16, t0 = (int)(tile / et) * 16;
-    const uint16_t* xr = a.x + (size_t)min(t0 + col, a.T - 1) * a.x_stride + 8 * lg;
-    const size_t wr = (size_t)min(e0 + col, a.E - 1) * a.H + 8 * lg;
-    v4f acc = {0.f, 0.f, 0.f, 0.f};
-    for (int k = 32 * wave; k < a.H; k += 128) {
-      const uint4 b = *reinterpret_cast<const uint4*>(xr + k);
-      if constexpr (kWF32) {
-        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.w) + wr + k);
-        const float4 u = p[0], v = p[1];
-        const float f[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-        uint4 t[3];
-        split3(f, t);
-#pragma unroll
-        for (int i = 0; i < 3; ++i) acc = mfma_bf16(t[i], b, acc);
-      } else {
-        acc = mfma_bf16(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.w) + wr + k), b, acc);
-      }
-    }
-    s_part[wave][lane] = acc;
-    __syncthreads();
-    if (wave == 0) {
-      const v4f sum = (s_part[0][lane] + s_part[1][lane]) + (s_part[2][lane] + s_part[3][lane]);
-      const int t = t0 + col, e = e0 + 4 * lg;
-      if (t < a.T) {
-        float* out = a.logits + (size_t)t * a.E + e;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (e + i < a.E) out[i] = sum[i];
-      }
-    }
-    __syncthreads();                               // the parts are read before the next tile's are written
+template <bool kWF32, int kM, int kN, int kW, int kSW, int kSX, int kP>
+hipError_t launch(const GateArgs& a, hipStream_t s) {
+  const int etiles = (a.E + 16 * kM - 1) / (16 * kM);
+  const long tiles = (long)etiles * (((long)a.T + 16 * kN - 1) / (16 * kN));
+  const long grid = (tiles + 7) / 8 * 8;
+  if (grid * 64 * kW > (long)UINT32_MAX) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL((k_gate<kWF32, kM, kN, kW, kSW, kSX, kP>), dim3((unsigned)grid), dim3(64 * kW), 0, s, a, etiles, tiles);
+  return hipGetLastError();
+}
+
+// The tile sizes built, in units of 16 experts and 16 tokens.  A workgroup fetches its rows of both
+// operands once, at 40 to 50 bytes a clock and compute unit whatever the tile, so the time goes as the bytes
+// of a tile's rows times the rounds its workgroups need on 256 compute units; the smallest product
+// wins, of equal ones the smaller tile.  Measured (BF16 weights, H 7168, E 256; us of the
+// chosen tile, next smaller, next larger): T 128 8.5, -, 10.5 (1 x 1); T 1024 13.4, 20.2, 17.8 (2 x 2); T 2048
+// 18.3, 25.2, 23.0 (4 x 2); T 4096 24.5, 34.6, 32.9 (4 x 4); T 8192 49.0, 63.4, - (8 x 4).
+struct Tile {
+  int m, n;
+};
+constexpr Tile kTilesBf16[] = {{1, 1}, {1, 2}, {2, 2}, {4, 2}, {4, 4}, {8, 4}};
+constexpr Tile kTilesF32[] = {{1, 1}, {1, 2}, {2, 2}, {2, 4}, {4, 8}};
+
+template <int kCount>
+int choose(const Tile (&tiles)[kCount], int weight_bytes, const GateArgs& a) {
+  int best = 0;
+  double least = 0;
+  for (int i = 0; i < kCount; ++i) {
+    const Tile t = tiles[i];
+    const long groups = (long)((a.E + 16 * t.m - 1) / (16 * t.m)) * (((long)a.T + 16 * t.n - 1) / (16 * t.n));
+    const double cost = (double)((groups + 255) / 256) * (t.m * weight_bytes + t.n * 2);
+    if (i == 0 || cost < least) best = i, least = cost;
   }
+  return best;
 }
 
 }  // namespace
 
 hipError_t launch_gate_logits(const GateArgs& a, hipStream_t s) {
-  const long tiles = (long)((a.E + 15) / 16) * ((a.T + 15) / 16);
-  const int grid = (int)(tiles < (1 << 20) ? tiles : (1 << 20));
-  if (a.w_f32) hipLaunchKernelGGL((k_gate<true>), dim3(grid), dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((k_gate<false>), dim3(grid), dim3(256), 0, s, a);
-  return hipGetLastError();
+  if (a.w_f32) {
+    switch (choose(kTilesF32, 4, a)) {
+      case 0: return launch<true, 1, 1, 8, 2, 2, 1>(a, s);
+      case 1: return launch<true, 1, 2, 8, 2, 2, 1>(a, s);
+      case 2: return launch<true, 2, 2, 8, 1, 1, 2>(a, s);
+      case 3: return launch<true, 2, 4, 8, 1, 1, 2>(a, s);
+      default: return launch<true, 4, 8, 4, 1, 1, 4>(a, s);
+    }
+  }
+  switch (choose(kTilesBf16, 2, a)) {
+    case 0: return launch<false, 1, 1, 8, 4, 4, 1>(a, s);
+    case 1: return launch<false, 1, 2, 8, 3, 3, 1>(a, s);
+    case 2: return launch<false, 2, 2, 8, 2, 2, 1>(a, s);
+    case 3: return launch<false, 4, 2, 8, 1, 2, 2>(a, s);
+    case 4: return launch<false, 4, 4, 8, 1, 1, 2>(a, s);
+    default: return launch<false, 8, 4, 4, 1, 2, 4>(a, s);
+  }
 }
 
 }  // namespace mm

@@ -354,7 +354,7 @@ typedef struct {
   int32_t weight_dtype;  /* mega_moe_dtype of w */
   uint32_t flags;        /* 0 */
   int64_t x_stride;      /* elements from one row of x to the next: 0 (= H), or >= H and a multiple
-                            of 8, < 2^40 */
+                            of 8, at most 2^22 */
 } mega_moe_gate_problem;
 
 /* Gate product: logits[t, e] = sum_h x[t, h] * w[e, h], products exact, sums in float32.

@@ -74,7 +74,7 @@ def _gp(T=4, H=256, E=8, **kw):
 
 @pytest.mark.parametrize("kw", [dict(T=-1), dict(T=1 << 30), dict(H=0), dict(H=200), dict(H=16512), dict(E=0),
                                 dict(E=8193), dict(weight_dtype=2), dict(flags=1), dict(x_stride=248),
-                                dict(x_stride=260), dict(x_stride=-8)])
+                                dict(x_stride=260), dict(x_stride=-8), dict(x_stride=(1 << 22) + 8)])
 def test_gate_refuses_bad_problems(kw):
     assert _gate(_gp(**kw)) == INVALID
 
@@ -93,6 +93,7 @@ def test_gate_refuses_bad_pointers():
 @cpu_only
 def test_gate_accepts():
     _accepted(_gate(_gp(E=3, x_stride=264)))
+    _accepted(_gate(_gp(T=1, x_stride=1 << 22)))
 
 
 def _topk(p, logits=1 * MB, bias=2 * MB, num_valid=3 * MB + 4, idx=4 * MB, w=5 * MB):
