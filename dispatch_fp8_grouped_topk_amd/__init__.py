@@ -1,7 +1,8 @@
 """Python binding of libmegamoe, the MI355X (gfx950) MegaMoE expert-layer library.
 
 Argument marshalling only: torch tensors are passed to the C ABI (include/mega_moe.h) as raw
-device pointers together with the current HIP stream; every step of the layer runs in the
+device pointers together with the current HIP stream (through ctypes; for the operators in front
+of the layer through the compiled module _binding); every step of the layer runs in the
 library's HIP kernels.  There is no fallback: if the shared library is missing or fails to
 load, importing the binding's functions raises.
 
@@ -445,42 +446,24 @@ def mega_moe_diag_mfma_block_sums(fmt: int, a, b, a_scale=None, b_scale=None, st
     return out
 
 
-def _dtype_of(code):
-    import torch
-    return {DTYPE_BF16: torch.bfloat16, DTYPE_F32: torch.float32}.get(code)
+_binding_module = None
 
 
-def _check_rows(name, t, device, dtype, shape, stride):
-    """A [T, n] tensor whose rows are `stride` elements apart (0: n), as the problem says."""
-    if t.dtype != dtype or t.shape != shape or t.device != device:
-        raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}, expected {dtype} {shape} on {device}")
-    if shape[0] and shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError(f"the rows of {name} must be contiguous")
-    if shape[0] > 1 and t.stride(0) != (stride or shape[1]):
-        raise ValueError(f"the rows of {name} are {t.stride(0)} elements apart, the problem says {stride or shape[1]}")
+def _compiled():
+    """The compiled part of the binding (argument checks of the operators in front of the layer)."""
+    global _binding_module
+    if _binding_module is None:
+        _load()                              # torch and the library it links to
+        from . import _binding as module
+        _binding_module = module
+    return _binding_module
 
 
-def _check_buffer(name, t, device, dtype, shape):
-    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}, expected {dtype} {shape}, contiguous, "
-                         f"on {device}")
-
-
-def _front_call(what, fn, problem, device, ptrs, stream):
-    """Call an operator in front of the layer with `device` current, on `stream` or its current stream."""
-    import torch
-    index = device.index
+def _handle(stream):
+    """A stream argument as the binding takes it: None (the current stream) or an int."""
     if stream is None:
-        handle = torch.cuda.current_stream(device).cuda_stream
-    else:
-        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if index == torch.cuda.current_device():
-        st = fn(ctypes.byref(problem), *ptrs, handle)
-    else:
-        with torch.cuda.device(index):
-            st = fn(ctypes.byref(problem), *ptrs, handle)
-    if st:
-        raise MegaMoEError(st, what)
+        return None
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def mega_moe_norm_quant(problem: NormProblem, x, weight, residual=None, residual_out=None, normed=None, q=None,
@@ -489,45 +472,18 @@ def mega_moe_norm_quant(problem: NormProblem, x, weight, residual=None, residual
     x, residual, residual_out: [T, H] of the problem's x_dtype with its row strides; weight [H];
     outputs normed bf16 [T, H], q uint8 [T, H] with q_sf float32 [T, H/128] or uint8 [T, H/32], each
     caller-allocated or None."""
-    import torch
-    dev = x.device
-    if dev.type != "cuda":
-        raise ValueError("mega_moe_norm_quant needs device tensors")
-    T, H = problem.num_tokens, problem.hidden
-    xt, wt = _dtype_of(problem.x_dtype), _dtype_of(problem.weight_dtype)
-    _check_rows("x", x, dev, xt, (T, H), problem.x_stride)
-    _check_buffer("weight", weight, dev, wt, (H,))
-    if residual is not None:
-        _check_rows("residual", residual, dev, xt, (T, H), problem.residual_stride)
-    if residual_out is not None:
-        _check_rows("residual_out", residual_out, dev, xt, (T, H), problem.residual_stride)
-    if normed is not None:
-        _check_buffer("normed", normed, dev, torch.bfloat16, (T, H))
-    if q is not None:
-        _check_buffer("q", q, dev, torch.uint8, (T, H))
-    if q_sf is not None:
-        if problem.recipe == RECIPE_FP8_B128:
-            _check_buffer("q_sf", q_sf, dev, torch.float32, (T, H // 128))
-        else:
-            _check_buffer("q_sf", q_sf, dev, torch.uint8, (T, H // 32))
-    _front_call("mega_moe_norm_quant", _load().mega_moe_norm_quant, problem, dev,
-                [None if t is None else t.data_ptr() for t in (x, residual, weight, residual_out, normed, q, q_sf)],
-                stream)
+    st = (_binding_module or _compiled()).norm_quant(problem, x, weight, residual, residual_out, normed, q, q_sf,
+                                                    _handle(stream))
+    if st:
+        raise MegaMoEError(st, "mega_moe_norm_quant")
 
 
 def mega_moe_gate_logits(problem: GateProblem, x, weight, logits, stream=None) -> None:
     """logits[t, e] = sum_h x[t, h] weight[e, h]: x bf16 [T, H], weight [E, H] of the problem's
     weight_dtype, logits float32 [T, E] (caller-allocated)."""
-    import torch
-    dev = x.device
-    if dev.type != "cuda":
-        raise ValueError("mega_moe_gate_logits needs device tensors")
-    T, H, E = problem.num_tokens, problem.hidden, problem.num_experts
-    _check_rows("x", x, dev, torch.bfloat16, (T, H), problem.x_stride)
-    _check_buffer("weight", weight, dev, _dtype_of(problem.weight_dtype), (E, H))
-    _check_buffer("logits", logits, dev, torch.float32, (T, E))
-    _front_call("mega_moe_gate_logits", _load().mega_moe_gate_logits, problem, dev,
-                (x.data_ptr(), weight.data_ptr(), logits.data_ptr()), stream)
+    st = (_binding_module or _compiled()).gate_logits(problem, x, weight, logits, _handle(stream))
+    if st:
+        raise MegaMoEError(st, "mega_moe_gate_logits")
 
 
 def mega_moe_gate_topk(problem: TopkProblem, logits, topk_idx, topk_w, bias=None, num_valid=None,
@@ -535,22 +491,10 @@ def mega_moe_gate_topk(problem: TopkProblem, logits, topk_idx, topk_w, bias=None
     """Choice of experts from logits [T, E] (include/mega_moe.h): topk_idx int32 and topk_w float32
     [T, topk + num_shared] (caller-allocated), bias float32 [E] or None, num_valid int32 [1] on the device
     or None."""
-    import torch
-    dev = logits.device
-    if dev.type != "cuda":
-        raise ValueError("mega_moe_gate_topk needs device tensors")
-    T, E = problem.num_tokens, problem.num_experts
-    cols = problem.topk + problem.num_shared
-    _check_rows("logits", logits, dev, _dtype_of(problem.logits_dtype), (T, E), problem.logits_stride)
-    if bias is not None:
-        _check_buffer("bias", bias, dev, torch.float32, (E,))
-    if num_valid is not None:
-        _check_buffer("num_valid", num_valid, dev, torch.int32, (1,))
-    _check_buffer("topk_idx", topk_idx, dev, torch.int32, (T, cols))
-    _check_buffer("topk_w", topk_w, dev, torch.float32, (T, cols))
-    _front_call("mega_moe_gate_topk", _load().mega_moe_gate_topk, problem, dev,
-                (logits.data_ptr(), None if bias is None else bias.data_ptr(),
-                 None if num_valid is None else num_valid.data_ptr(), topk_idx.data_ptr(), topk_w.data_ptr()), stream)
+    st = (_binding_module or _compiled()).gate_topk(problem, logits, topk_idx, topk_w, bias, num_valid,
+                                                   _handle(stream))
+    if st:
+        raise MegaMoEError(st, "mega_moe_gate_topk")
 
 
 class MegaMoE:

@@ -1,8 +1,9 @@
-"""Build libmegamoe.so (all HIP sources of csrc/) for gfx950 with hipcc, in place.
+"""Build libmegamoe.so (all HIP sources of csrc/) for gfx950 with hipcc, in place, and the compiled
+part of the Python binding, _binding.so (csrc/mm_binding.cpp, host code against torch's headers).
 
     python -m dispatch_fp8_grouped_topk_amd.build
 
-Compiles every translation unit in parallel into _build/ and links the shared library
+Compiles every translation unit in parallel into _build/ and links the shared libraries
 next to this file.  Always recompiles (it is the package's "does it build" check).
 """
 from __future__ import annotations
@@ -17,6 +18,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmegamoe.so")
+BINDING = os.path.join(HERE, "_binding.so")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
@@ -44,10 +46,37 @@ def _compile(src):
     return obj
 
 
+def _compile_binding():
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths
+    obj = os.path.join(BUILD, "mm_binding.cpp.o")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-w",
+           "-D__HIP_PLATFORM_AMD__", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", os.path.join(ROOT, "include"),
+           *[a for d in [*include_paths("cuda"), sysconfig.get_paths()["include"]] for a in ("-isystem", d)],
+           "-c", os.path.join(CSRC, "mm_binding.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compiling the binding failed:\n{r.stderr}")
+    return obj, os.path.join(os.path.dirname(torch.__file__), "lib")
+
+
+def _link_binding(obj, torch_lib):
+    tmp = BINDING + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-fPIC", obj, "-L", HERE, "-lmegamoe", "-L", torch_lib, "-lc10", "-lc10_hip",
+           "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN", "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"linking the binding failed:\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(verbose: bool = True) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(_compile, srcs))
     tmp = LIB + ".tmp"
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp]
@@ -55,6 +84,7 @@ def build(verbose: bool = True) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(*binding.result())
     if verbose:
         print(f"built {LIB} from {len(srcs)} sources", file=sys.stderr)
     return LIB

@@ -145,12 +145,9 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         mm.mega_moe_gate_logits(_gp(), x, x, x)
     with pytest.raises(ValueError, match="device tensors"):
         mm.mega_moe_gate_topk(_tp(), x, x, x)
-    cpu = torch.device("cpu")
-    ok = torch.zeros(4, 300)[:, :256]
-    mm._check_rows("x", ok, cpu, torch.float32, (4, 256), 300)
-    mm._check_rows("x", ok[:1], cpu, torch.float32, (1, 256), 0)      # one row has no stride
-    for bad in (ok.double(), ok[:3], torch.zeros(256, 4).t(), torch.zeros(4, 256)):
-        with pytest.raises(ValueError):
-            mm._check_rows("x", bad, cpu, torch.float32, (4, 256), 300)
-    with pytest.raises(ValueError):
-        mm._check_buffer("q", ok, cpu, torch.float32, (4, 256))
+    with pytest.raises(ValueError, match="must be a tensor"):
+        mm.mega_moe_norm_quant(_np(), x, None, normed=x)
+    with pytest.raises(ValueError, match="problem structure"):
+        mm.mega_moe_norm_quant(_gp(), x, x[0], normed=x)
+    with pytest.raises(ValueError, match="problem structure"):
+        mm.mega_moe_gate_topk(None, x, x, x)
