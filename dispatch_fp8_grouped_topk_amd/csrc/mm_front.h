@@ -46,6 +46,39 @@ struct TopkArgs {
   float scale, shared_weight;
 };
 
+// Lanes of a wave by DPP: v of the lane that kCtrl names (0 where there is none).
+template <int kCtrl>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kCtrl, 0xF, 0xF, true);
+}
+template <int kCtrl>
+__device__ __forceinline__ double dpp(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, (uint64_t)dpp<kCtrl>((uint32_t)u) | (uint64_t)dpp<kCtrl>((uint32_t)(u >> 32)) << 32);
+}
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140;   // quad_perm, row_*mirror
+constexpr int kBcast15 = 0x142, kBcast31 = 0x143, kShl = 0x100;                   // row_bcast, row_shl:n
+
+// The sum / the largest over the 64 lanes, in lane 63.
+__device__ __forceinline__ double wave_sum63(double v) {
+  v += dpp<kXor1>(v);
+  v += dpp<kXor2>(v);
+  v += dpp<kHalfMirror>(v);
+  v += dpp<kMirror>(v);
+  const double rows = dpp<kBcast15>(v);            // lane 15 -> row 1, lane 31 -> row 2, lane 47 -> row 3
+  v += (threadIdx.x & 16) ? rows : 0.0;            // rows 1 and 3
+  const double half = dpp<kBcast31>(v);            // lane 31 -> rows 2 and 3
+  return v + ((threadIdx.x & 32) ? half : 0.0);
+}
+__device__ __forceinline__ uint32_t wave_max63(uint32_t v) {
+  v = max(v, dpp<kXor1>(v));
+  v = max(v, dpp<kXor2>(v));
+  v = max(v, dpp<kHalfMirror>(v));
+  v = max(v, dpp<kMirror>(v));
+  v = max(v, dpp<kBcast15>(v));                    // lanes without a source read 0
+  return max(v, dpp<kBcast31>(v));
+}
+
 hipError_t launch_norm_quant(const NormArgs& a, hipStream_t s);
 hipError_t launch_gate_logits(const GateArgs& a, hipStream_t s);
 hipError_t launch_gate_topk(const TopkArgs& a, hipStream_t s);

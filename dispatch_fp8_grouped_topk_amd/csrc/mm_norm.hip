@@ -28,30 +28,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, v);
 }
 
-template <int kCtrl>
-__device__ __forceinline__ uint32_t dpp(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kCtrl, 0xF, 0xF, true);
-}
-template <int kCtrl>
-__device__ __forceinline__ double dpp(double v) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, v);
-  return __builtin_bit_cast(double, (uint64_t)dpp<kCtrl>((uint32_t)u) | (uint64_t)dpp<kCtrl>((uint32_t)(u >> 32)) << 32);
-}
-constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140;   // quad_perm, row_*mirror
-constexpr int kBcast15 = 0x142, kBcast31 = 0x143, kShl = 0x100;                   // row_bcast, row_shl:n
-
-// The sum over the 64 lanes, in lane 63.
-__device__ __forceinline__ double wave_sum63(double v) {
-  v += dpp<kXor1>(v);
-  v += dpp<kXor2>(v);
-  v += dpp<kHalfMirror>(v);
-  v += dpp<kMirror>(v);
-  const double rows = dpp<kBcast15>(v);            // lane 15 -> row 1, lane 31 -> row 2, lane 47 -> row 3
-  v += (threadIdx.x & 16) ? rows : 0.0;            // rows 1 and 3
-  const double half = dpp<kBcast31>(v);            // lane 31 -> rows 2 and 3
-  return v + ((threadIdx.x & 32) ? half : 0.0);
-}
-
 // Largest of the bits of |v| over 4 neighbouring lanes / the 16 lanes of a row.  As unsigned
 // integers magnitudes order as their values do, with infinity and NaN above every number.
 __device__ __forceinline__ uint32_t max4(uint32_t m) {
