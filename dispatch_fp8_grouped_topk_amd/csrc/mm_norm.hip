@@ -5,9 +5,14 @@
 //   per group of 128: sf = amax/448, q = E4M3(v / sf); per 32: the UE8M0 code of the smallest power
 //   of two s with amax/s <= 448, q = E4M3(v / s)
 //
-// A thread holds chunks of 8 consecutive columns, chunk tid + i * blockDim.  A group of 128 columns
-// is then one 16-lane row of a wave and a group of 32 four neighbouring lanes, so group maxima are
-// DPP reductions without LDS.  H is a multiple of 128, so a 16-lane row is wholly in or out.
+// A workgroup takes a row; a thread holds chunks of 8 consecutive columns, chunk tid + i * blockDim.  A
+// group of 128 columns is then one 16-lane row of a wave and a group of 32 four neighbouring lanes, so
+// group maxima are DPP reductions without LDS.  H is a multiple of 128, so a 16-lane row is wholly in
+// or out.
+//
+// Bound by memory: T 8192, H 7168 (BF16 rows and residual, all outputs, 530 MB) takes 100.8 us, 5.26 TB/s,
+// against the 5.4 TB/s that a large copy reaches here.  A single row takes 3.4 us, of which an empty
+// launch is 2.
 //
 // Numerics: sums of squares and r are float64 (no overflow for any float32 h, and the power-of-two
 // scales below can be decided exactly); v is float32; each output is rounded once from it.  A UE8M0
@@ -44,24 +49,6 @@ constexpr uint32_t kInfBits = 0x7F800000u;
 
 __device__ __forceinline__ uint32_t mag(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
-template <bool kF32>
-__device__ __forceinline__ void load8(const void* base, size_t elem, float (&v)[8]) {
-  if constexpr (kF32) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + elem);
-    const float4 a = p[0], b = p[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  } else {
-    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + elem);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-  }
-}
-
 __device__ __forceinline__ uint4 pack_bf16x8(const float (&v)[8]) {
   return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
 }
@@ -93,25 +80,68 @@ __device__ __forceinline__ uint32_t ue8m0_ceil64(double r) {
   return (uint32_t)min(max(e, 0), 254);
 }
 
-template <bool kXF32, bool kWF32, bool kPer32, int kNC, int kMaxThreads>
-__global__ __launch_bounds__(kMaxThreads) void k_norm_quant(NormArgs a) {
-  __shared__ double s_part[2][kMaxThreads / 64];
+// Eight values as loaded.
+template <bool kF32>
+struct Raw {
+  uint4 v[kF32 ? 2 : 1];
+  __device__ __forceinline__ void load(const void* base, size_t elem) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(base) + elem * (kF32 ? 4 : 2));
+    v[0] = p[0];
+    if constexpr (kF32) v[1] = p[1];
+  }
+  __device__ __forceinline__ void values(float (&f)[8]) const {
+    if constexpr (kF32) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        f[4 * i] = __uint_as_float(v[i].x);
+        f[4 * i + 1] = __uint_as_float(v[i].y);
+        f[4 * i + 2] = __uint_as_float(v[i].z);
+        f[4 * i + 3] = __uint_as_float(v[i].w);
+      }
+    } else {
+      const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      }
+    }
+  }
+};
+
+template <bool kXF32, bool kWF32, bool kPer32, int kNC>
+__global__ __launch_bounds__(1024) void k_norm_quant(NormArgs a) {
+  __shared__ double s_part[2][16];
   const int chunks = a.H / 8, tid = threadIdx.x, waves = blockDim.x / 64;
   const double inv_h = 1.0 / a.H;
   int parity = 0;
   for (int row = blockIdx.x; row < a.T; row += gridDim.x, parity ^= 1) {
+    Raw<kXF32> x[kNC], r[kNC];
+    Raw<kWF32> wt[kNC];
+#pragma unroll
+    for (int i = 0; i < kNC; ++i) {
+      const int c = tid + i * blockDim.x;
+      if (c >= chunks) continue;
+      x[i].load(a.x, (size_t)row * a.x_stride + 8 * c);
+      if (a.residual) r[i].load(a.residual, (size_t)row * a.residual_stride + 8 * c);
+    }
+#pragma unroll
+    for (int i = 0; i < kNC; ++i) {                // asked for before the sum is known, used after it
+      const int c = tid + i * blockDim.x;
+      if (c < chunks) wt[i].load(a.weight, 8 * c);
+    }
     float h[kNC][8];
     double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < kNC; ++i) {
       const int c = tid + i * blockDim.x;
       if (c >= chunks) continue;
-      load8<kXF32>(a.x, (size_t)row * a.x_stride + 8 * c, h[i]);
+      x[i].values(h[i]);
       if (a.residual) {
-        float r[8];
-        load8<kXF32>(a.residual, (size_t)row * a.residual_stride + 8 * c, r);
+        float f[8];
+        r[i].values(f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) h[i][j] += r[j];
+        for (int j = 0; j < 8; ++j) h[i][j] += f[j];
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) sum = __builtin_fma((double)h[i][j], (double)h[i][j], sum);
@@ -128,7 +158,7 @@ __global__ __launch_bounds__(kMaxThreads) void k_norm_quant(NormArgs a) {
       const int c = tid + i * blockDim.x;
       if (c >= chunks) continue;
       float w[8], v[8];
-      load8<kWF32>(a.weight, 8 * c, w);
+      wt[i].values(w);
       if (a.residual_out) store8<kXF32>(a.residual_out, (size_t)row * a.residual_stride + 8 * c, h[i]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = h[i][j] * r32 * w[j];
@@ -178,12 +208,15 @@ __global__ __launch_bounds__(kMaxThreads) void k_norm_quant(NormArgs a) {
   }
 }
 
+// One chunk a thread as far as a workgroup's 1024 threads go, then two: fewer threads with four chunks each
+// were slower at every size (us with 1, 2, 4 chunks, H 7168: T 1 3.4, 3.5, 4.5; T 128 4.3, 4.5, 5.5; T 8192
+// 100.8, 105.2, 107.0), as more of a row's loads are under way and less follows the sum.
 template <bool kXF32, bool kWF32, bool kPer32>
 void launch(const NormArgs& a, hipStream_t s) {
   const int chunks = a.H / 8, grid = a.T < (1 << 20) ? a.T : (1 << 20);
-  const auto threads = [&](int nc) { return ((chunks + nc - 1) / nc + 63) / 64 * 64; };
-  if (chunks <= 1024) hipLaunchKernelGGL((k_norm_quant<kXF32, kWF32, kPer32, 4, 256>), dim3(grid), dim3(threads(4)), 0, s, a);
-  else hipLaunchKernelGGL((k_norm_quant<kXF32, kWF32, kPer32, 4, 512>), dim3(grid), dim3(threads(4)), 0, s, a);
+  const int per = chunks <= 1024 ? 1 : 2, threads = ((chunks + per - 1) / per + 63) / 64 * 64;
+  if (per == 1) hipLaunchKernelGGL((k_norm_quant<kXF32, kWF32, kPer32, 1>), dim3(grid), dim3(threads), 0, s, a);
+  else hipLaunchKernelGGL((k_norm_quant<kXF32, kWF32, kPer32, 2>), dim3(grid), dim3(threads), 0, s, a);
 }
 
 }  // namespace
