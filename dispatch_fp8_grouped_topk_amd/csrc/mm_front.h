@@ -57,7 +57,12 @@ __device__ __forceinline__ double dpp(double v) {
   return __builtin_bit_cast(double, (uint64_t)dpp<kCtrl>((uint32_t)u) | (uint64_t)dpp<kCtrl>((uint32_t)(u >> 32)) << 32);
 }
 constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140;   // quad_perm, row_*mirror
-constexpr int kBcast15 = 0x142, kBcast31 = 0x143, kShl = 0x100;                   // row_bcast, row_shl:n
+constexpr int kBcast15 = 0x142, kBcast31 = 0x143, kShl = 0x100, kRor = 0x120;     // row_bcast, row_shl:n, row_ror:n
+
+template <int kCtrl>
+struct Ctrl {
+  static constexpr int value = kCtrl;
+};
 
 // The sum / the largest over the 64 lanes, in lane 63.
 __device__ __forceinline__ double wave_sum63(double v) {
@@ -69,6 +74,17 @@ __device__ __forceinline__ double wave_sum63(double v) {
   v += (threadIdx.x & 16) ? rows : 0.0;            // rows 1 and 3
   const double half = dpp<kBcast31>(v);            // lane 31 -> rows 2 and 3
   return v + ((threadIdx.x & 32) ? half : 0.0);
+}
+__device__ __forceinline__ float wave_sum63(float v) {
+  const auto from = [](float u, auto ctrl) { return __uint_as_float(dpp<decltype(ctrl)::value>(__float_as_uint(u))); };
+  v += from(v, Ctrl<kXor1>{});
+  v += from(v, Ctrl<kXor2>{});
+  v += from(v, Ctrl<kHalfMirror>{});
+  v += from(v, Ctrl<kMirror>{});
+  const float rows = from(v, Ctrl<kBcast15>{});
+  v += (threadIdx.x & 16) ? rows : 0.f;
+  const float half = from(v, Ctrl<kBcast31>{});
+  return v + ((threadIdx.x & 32) ? half : 0.f);
 }
 __device__ __forceinline__ uint32_t wave_max63(uint32_t v) {
   v = max(v, dpp<kXor1>(v));

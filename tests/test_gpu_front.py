@@ -284,10 +284,12 @@ def _topk(logits, k, bias=None, num_valid=None, stream=None, **kw):
     return idx[:T * cols].view(T, cols), w[:T * cols].view(T, cols)
 
 
-def _check_topk(logits, k, bias=None, num_valid=None, **kw):
-    idx, w = _topk(logits, k, bias, num_valid, **kw)
+def _check_topk(logits, k, bias=None, num_valid=None, times=1, **kw):
+    """times: the rows that many times over (large batches take another kernel)."""
+    idx, w = _topk(logits.repeat(times, 1) if times > 1 else logits, k, bias, num_valid, **dict(kw))
     ref_i, ref_w = front.gate_topk(_f64(logits), None if bias is None else _f64(bias), k,
                                    num_valid=None if num_valid is None else int(num_valid.item()), **kw)
+    ref_i, ref_w = np.tile(ref_i, (times, 1)), np.tile(ref_w, (times, 1))
     got_i = idx.cpu().numpy()
     assert np.array_equal(got_i, ref_i), f"rows {np.unique(np.argwhere(got_i != ref_i)[:, 0])[:8]} differ"
     got_w = _f64(w)
@@ -332,10 +334,38 @@ def test_topk_groups(T, E, k, G, KG, group_top, biased, score):
     _check_topk(logits, k, bias, score=score, num_groups=G, topk_groups=KG, group_top=group_top, renorm=True)
 
 
+LARGE = [(8201, 256, 8, 8, 4, 2), (8192, 256, 8, 1, 1, 1), (4099, 64, 6, 1, 1, 1), (4100, 128, 14, 16, 5, 2),
+         (9000, 200, 3, 5, 2, 1), (4097, 24, 1, 8, 1, 2), (4096, 96, 15, 3, 2, 1), (4500, 7, 7, 1, 1, 1),
+         (5000, 130, 12, 13, 4, 2)]
+
+
+@pytest.mark.parametrize("dtype,pad", [("f32", 0), ("bf16", 1)])
+@pytest.mark.parametrize("score,biased", [("softmax", False), ("softmax", True), ("sigmoid", True)])
+@pytest.mark.parametrize("T,E,k,G,KG,group_top", LARGE)
+def test_topk_large_batches(T, E, k, G, KG, group_top, score, biased, dtype, pad):
+    _say("topk large", T, E, k, G, KG, group_top, score, biased, dtype)
+    g = torch.Generator().manual_seed(T + E)
+    rows = 331                                                # different ones; the oracle goes row by row
+    logits = (torch.randn(rows, E, generator=g) * 1.5).to(DT[dtype][1])
+    bias = (torch.randn(E, generator=g) * 0.1).cuda() if biased else None
+    big = _rows(logits.repeat(T // rows + 1, 1)[:T].cuda(), pad)
+    kw = dict(score=score, num_groups=G, topk_groups=KG, group_top=group_top, renorm=True)
+    n = T - 9
+    idx, w = _topk(big, k, bias, torch.tensor([n], dtype=torch.int32, device="cuda"),
+                   num_shared=1 if k < 14 else 0, **dict(kw))
+    ref_i, ref_w = front.gate_topk(_f64(logits), None if bias is None else _f64(bias), k,
+                                   num_shared=1 if k < 14 else 0, **kw)
+    of = np.arange(n) % rows
+    assert np.array_equal(idx[:n].cpu().numpy(), ref_i[of])
+    assert (np.abs(_f64(w[:n]) - ref_w[of]) <= 2.0 ** -18 * ref_w[of] + 2.0 ** -120).all()
+    assert (idx[n:] == -1).all() and (w[n:] == 0).all()
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("biased", [False, True])
 @pytest.mark.parametrize("G,KG,group_top", [(1, 1, 1), (8, 3, 1), (8, 3, 2)])
-def test_topk_ties_and_close_scores(G, KG, group_top, biased, score):
+@pytest.mark.parametrize("times", [1, 65])
+def test_topk_ties_and_close_scores(times, G, KG, group_top, biased, score):
     """Equal logits, logits one float32 step apart and scores that round to the same float32."""
     g = torch.Generator().manual_seed(11)
     T, E, k = 64, 64, 9
@@ -346,17 +376,18 @@ def test_topk_ties_and_close_scores(G, KG, group_top, biased, score):
     logits[32:48] = 20 + steps[32:48].float()                 # sigmoid within 2^-28 of 1
     logits[48:] = 0
     bias = (torch.randint(0, 2, (E,), generator=g).float() * 0.25).cuda() if biased else None
-    _check_topk(logits.cuda(), k, bias, score=score, num_groups=G, topk_groups=KG, group_top=group_top)
+    _check_topk(logits.cuda(), k, bias, times=times, score=score, num_groups=G, topk_groups=KG, group_top=group_top)
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("biased", [False, True])
 @pytest.mark.parametrize("G,KG,group_top", [(1, 1, 1), (4, 2, 1), (4, 2, 2)])
-def test_topk_scores_a_rounding_apart(G, KG, group_top, biased, score):
+@pytest.mark.parametrize("E,times", [(32, 1), (32, 21), (256, 1), (256, 41)])
+def test_topk_scores_a_rounding_apart(E, times, G, KG, group_top, biased, score):
     """Scores that differ by less than a float32 exponential is off: logits spread over a few hundred
     steps around one value, with biases that nearly cancel the difference of two levels."""
     g = torch.Generator().manual_seed(12)
-    T, E, k = 200, 32, 8
+    T, k = 200, 8
     step = torch.randint(-300, 300, (T, E), generator=g).double() * 2.0 ** -24
     logits = (0.7 + step).float()
     bias = None
@@ -368,15 +399,16 @@ def test_topk_scores_a_rounding_apart(G, KG, group_top, biased, score):
             bias = torch.where(high, torch.zeros(()), (s[0] - s[1]).float()).cuda()
         else:
             bias = (torch.randint(0, 2, (E,), generator=g).float() * 2.0 ** -26).cuda()
-    _check_topk(logits.cuda(), k, bias, score=score, num_groups=G, topk_groups=KG, group_top=group_top)
+    _check_topk(logits.cuda(), k, bias, times=times, score=score, num_groups=G, topk_groups=KG, group_top=group_top)
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("G,KG,group_top", [(1, 1, 1), (4, 2, 1), (4, 2, 2)])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-def test_topk_masked_experts(dtype, G, KG, group_top, score):
+@pytest.mark.parametrize("E,times", [(32, 1), (32, 342), (256, 1), (256, 683), (1024, 1)])
+def test_topk_masked_experts(E, times, dtype, G, KG, group_top, score):
     g = torch.Generator().manual_seed(13)
-    E, k = 32, 6
+    k = 6
     logits = torch.randn(12, E, generator=g)
     low = torch.finfo(DT[dtype][1]).min
     logits[1] = -float("inf")                                  # nothing to choose
@@ -389,14 +421,14 @@ def test_topk_masked_experts(dtype, G, KG, group_top, score):
     logits[8, 8:16] = -float("inf")                            # a whole group
     logits[9] = -200.0                                         # scores beyond float32's range
     logits[9, 4], logits[9, 20] = -199.0, -150.0
-    logits[10, :31] = -float("inf")
+    logits[10, :E - 1] = -float("inf")
     logits = logits.to(DT[dtype][1]).cuda()
     bias = torch.zeros(E)
     bias[2], bias[17], bias[30], bias[9] = float("nan"), -float("inf"), float("inf"), 0.5
     for b in (None, bias.cuda()):
         for renorm in (False, True):
-            _check_topk(logits, k, b, score=score, num_groups=G, topk_groups=KG, group_top=group_top, renorm=renorm,
-                        num_shared=1)
+            _check_topk(logits, k, b, times=times, score=score, num_groups=G, topk_groups=KG, group_top=group_top,
+                        renorm=renorm, num_shared=1)
 
 
 @pytest.mark.parametrize("n", [-3, 0, 1, 30, 37, 100])
