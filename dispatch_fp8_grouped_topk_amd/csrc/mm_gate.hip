@@ -56,7 +56,8 @@ __device__ __forceinline__ void wait_vmcnt() {
   __builtin_amdgcn_s_waitcnt((kN & 0xF) | ((kN >> 4) << 14) | (0x7 << 4) | (0xF << 8));
 }
 
-// One workgroup per tile of 16 kM experts x 16 kN tokens.  Its kW waves share K: wave w takes the
+// One workgroup per tile of kE experts x kT tokens (each 8, which fills half an MFMA operand, or a
+// multiple of 16).  Its kW waves share K: wave w takes the
 // steps of 64 columns w, w + kW, ..., each for the whole tile, through a ring of its own in LDS (kSW
 // steps of weights, kSX of tokens), so the loop has no barrier; the waves' sums meet in LDS at the end.
 // A step's weights are taken in kP parts: while one part is multiplied the next one is read into
@@ -66,32 +67,40 @@ __device__ __forceinline__ void wait_vmcnt() {
 // registers touch 64 bytes of 16 rows, and the L2 delivers lines, half of each for nothing.
 // In LDS a row's eight 16-byte chunks are permuted by (row / 2) % 8, so that the 16 rows of an
 // operand read fall into different banks.
-template <bool kWF32, int kM, int kN, int kW, int kSW, int kSX, int kP>
-__global__ __launch_bounds__(64 * kW) void k_gate(GateArgs a, int etiles, long tiles) {
+template <bool kWF32, int kE, int kT, int kW, int kSW, int kSX, int kP>
+__global__ __launch_bounds__(64 * kW) void k_gate(GateArgs a, int etiles, int ttiles, int experts_first) {
   constexpr int kWB = kWF32 ? 4 : 2;                     // bytes a weight
   constexpr int kHalves = kWF32 ? 2 : 1;                 // 128-byte lines of a weight row in a step
-  constexpr int kMP = kM / kP;                           // operands of 16 experts in a part
-  constexpr int kLX = 2 * kN, kLP = 2 * kMP * kHalves, kLW = kP * kLP;   // loads of a step / part
+  constexpr int kM = (kE + 15) / 16, kN = (kT + 15) / 16, kMP = kM / kP;   // MFMA operands of a tile, of a part
+  constexpr int kRows = kE / 8 / kP;                     // loads of eight weight rows in a part
+  constexpr int kLX = kT / 8, kLP = kRows * kHalves, kLW = kP * kLP;       // loads of a step, of a part
   // Loads issued since a part's own when it is waited for (a step's tokens go out with its part 0):
   // the rest of that step, the steps between, and what the present step has issued before this part.
   static_assert(kSX >= kSW && kM % kP == 0 && (kP == 1 || kP % 2 == 0), "");
   constexpr int kLater0 = kLW - kLP + (kSW - 1) * (kLX + kLW), kLater = kLater0 + kLX;
   static_assert(kLater < 64, "vmcnt holds 6 bits");
+  // A tile of 8 x 8 fills an MFMA with both halves of a step: rows and columns 0 .. 7 are its experts and tokens at
+  // columns 0 .. 31, rows and columns 8 .. 15 the same at columns 32 .. 63, and the sums of the two
+  // diagonal quarters are added at the end.
+  constexpr bool kFolded = kE == 8 && kT == 8;
+  constexpr int kSubs = kFolded ? 1 : 2;                 // MFMA steps of a step
   constexpr int kXBytes = kLX * 1024, kWBytes = kLW * 1024;
   constexpr int kRing = kSX * kXBytes + kSW * kWBytes;   // a wave's LDS
   constexpr int kSums = kM * kN * 1024;                  // a wave's sums
   __shared__ __align__(1024) char lds[kW * (kRing > kSums ? kRing : kSums)];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 15, lg = lane >> 4;
   const int per = gridDim.x >> 3;
-  const long tile = (long)(blockIdx.x & 7) * per + (blockIdx.x >> 3);   // each XCD walks neighbouring tiles
-  if (tile >= tiles) return;
-  const int e0 = (int)(tile % etiles) * 16 * kM;
-  const long t0 = tile / etiles * 16 * kN;
+  // Each XCD walks neighbouring tiles: either all expert tiles of a few token tiles, or all token
+  // tiles of a few expert tiles.
+  const long tile = (long)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  if (tile >= (long)etiles * ttiles) return;
+  const int e0 = (int)(experts_first ? tile % etiles : tile / ttiles) * kE;
+  const long t0 = (experts_first ? tile / etiles : tile % ttiles) * kT;
   char* ring = lds + wave * kRing;
 
   // buffers of this tile's rows (at most 2^30 bytes): rows past the last one are out of range and read
   // zeros, or repeat the first ones; neither is stored
-  const int erows = min(16 * kM, a.E - e0), trows = (int)min((long)(16 * kN), a.T - t0);
+  const int erows = min(kE, a.E - e0), trows = (int)min((long)kT, a.T - t0);
   const uint32_t wstride = (uint32_t)a.H * kWB, xstride = (uint32_t)(a.x_stride * 2);
   const rsrc_t wr = make_rsrc(static_cast<const char*>(a.w) + (size_t)e0 * wstride, (size_t)erows * wstride);
   const rsrc_t xr = make_rsrc(a.x + (size_t)t0 * a.x_stride, (size_t)(trows - 1) * xstride + (size_t)a.H * 2);
@@ -105,8 +114,12 @@ __global__ __launch_bounds__(64 * kW) void k_gate(GateArgs a, int etiles, long t
     wlane[o] = (uint32_t)sub * wstride + chunk;
     xlane[o] = (uint32_t)sub * xstride + chunk;
   }
-  // operand reads: row col, chunk c of its line
-  const auto chunk_at = [&](int c) { return col * 128 + ((c ^ (col >> 1)) * 16); };
+  // operand reads: row col, chunk c of its line; a tile of eight rows is read twice over, or folded
+  const auto chunk_at = [&](int c, int rows) {
+    const int r = rows == 8 ? col & 7 : col;
+    return r * 128 + ((c ^ (r >> 1)) * 16);
+  };
+  const auto half_at = [&](int s) { return kFolded ? col >> 3 : s; };
 
   const int all = a.H / 64, steps = all > wave ? (all - wave + kW - 1) / kW : 0;
   // Out of range is what lies at or past the buffer's size less the scalar offset, so the scalar offset
@@ -120,39 +133,39 @@ __global__ __launch_bounds__(64 * kW) void k_gate(GateArgs a, int etiles, long t
     const uint32_t k = column(i) * (128 * kHalves), out = beyond(i);
     char* to = ring + kSX * kXBytes + slot * kWBytes + p * kLP * 1024;
 #pragma unroll
-    for (int m = 0; m < 2 * kMP; ++m)
+    for (int m = 0; m < kRows; ++m)
 #pragma unroll
       for (int h = 0; h < kHalves; ++h)
-        lds_load16(wr, wlane[m & 1] + out, k + 128 * h + rows_at(8 * (2 * kMP * p + m), erows, wstride),
-                   to + (h * 2 * kMP + m) * 1024);
+        lds_load16(wr, wlane[m & 1] + out, k + 128 * h + rows_at(8 * (kRows * p + m), erows, wstride),
+                   to + (h * kRows + m) * 1024);
   };
   const auto fetch_x = [&](int i, int slot) {
     const uint32_t k = column(i) * 128, out = beyond(i);
     char* to = ring + slot * kXBytes;
 #pragma unroll
-    for (int n = 0; n < 2 * kN; ++n) lds_load16(xr, xlane[n & 1] + out, k + rows_at(8 * n, trows, xstride), to + n * 1024);
+    for (int n = 0; n < kLX; ++n) lds_load16(xr, xlane[n & 1] + out, k + rows_at(8 * n, trows, xstride), to + n * 1024);
   };
 
-  v4i X[2][2][kN], W[2][2][kMP][kHalves];
-  const auto read_x = [&](int slot, v4i (&to)[2][kN]) {
+  v4i X[2][kSubs][kN], W[2][kSubs][kMP][kHalves];
+  const auto read_x = [&](int slot, v4i (&to)[kSubs][kN]) {
     const char* xs = ring + slot * kXBytes;
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
+    for (int s = 0; s < kSubs; ++s)
 #pragma unroll
-      for (int n = 0; n < kN; ++n) to[s][n] = *reinterpret_cast<const v4i*>(xs + n * 2048 + chunk_at(4 * s + lg));
+      for (int n = 0; n < kN; ++n) to[s][n] = *reinterpret_cast<const v4i*>(xs + n * 2048 + chunk_at(4 * half_at(s) + lg, kT));
   };
-  const auto read_w = [&](int slot, int p, v4i (&to)[2][kMP][kHalves]) {
+  const auto read_w = [&](int slot, int p, v4i (&to)[kSubs][kMP][kHalves]) {
     const char* ws = ring + kSX * kXBytes + slot * kWBytes + p * kLP * 1024;
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
+    for (int s = 0; s < kSubs; ++s)
 #pragma unroll
       for (int m = 0; m < kMP; ++m) {
         if constexpr (kWF32) {
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            to[s][m][h] = *reinterpret_cast<const v4i*>(ws + (s * 2 * kMP + 2 * m) * 1024 + chunk_at(2 * lg + h));
+            to[s][m][h] = *reinterpret_cast<const v4i*>(ws + (half_at(s) * kRows + 2 * m) * 1024 + chunk_at(2 * lg + h, kE));
         } else {
-          to[s][m][0] = *reinterpret_cast<const v4i*>(ws + m * 2048 + chunk_at(4 * s + lg));
+          to[s][m][0] = *reinterpret_cast<const v4i*>(ws + m * 2048 + chunk_at(4 * half_at(s) + lg, kE));
         }
       }
   };
@@ -200,7 +213,7 @@ __global__ __launch_bounds__(64 * kW) void k_gate(GateArgs a, int etiles, long t
           }
           __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-          for (int s = 0; s < 2; ++s)
+          for (int s = 0; s < kSubs; ++s)
 #pragma unroll
             for (int m = 0; m < kMP; ++m)
 #pragma unroll
@@ -236,9 +249,13 @@ __global__ __launch_bounds__(64 * kW) void k_gate(GateArgs a, int etiles, long t
     v4f sum = sums[j * 64 + lane];
 #pragma unroll
     for (int w = 1; w < kW; ++w) sum += sums[(w * kM * kN + j) * 64 + lane];
+    if constexpr (kFolded) {                       // the lane of row + 8, column + 8
+#pragma unroll
+      for (int w = 0; w < kW; ++w) sum += sums[w * 64 + ((lane + 40) & 63)];
+    }
     const int e = e0 + 16 * (j / kN) + 4 * lg;
     const long t = t0 + 16 * (j % kN) + col;
-    if (t >= a.T) continue;
+    if (t >= a.T || (kE == 8 && lg >= 2) || (kT == 8 && col >= 8)) continue;
     float* out = a.logits + (size_t)t * a.E + e;
     if ((a.E & 3) == 0) {
       if (e < a.E) *reinterpret_cast<v4f*>(out) = sum;
@@ -250,27 +267,30 @@ __global__ __launch_bounds__(64 * kW) void k_gate(GateArgs a, int etiles, long t
   }
 }
 
-template <bool kWF32, int kM, int kN, int kW, int kSW, int kSX, int kP>
+template <bool kWF32, int kE, int kT, int kW, int kSW, int kSX, int kP>
 hipError_t launch(const GateArgs& a, hipStream_t s) {
-  const int etiles = (a.E + 16 * kM - 1) / (16 * kM);
-  const long tiles = (long)etiles * (((long)a.T + 16 * kN - 1) / (16 * kN));
-  const long grid = (tiles + 7) / 8 * 8;
+  const int etiles = (a.E + kE - 1) / kE, ttiles = (int)(((long)a.T + kT - 1) / kT);
+  const long grid = ((long)etiles * ttiles + 7) / 8 * 8;
+  // an XCD's L2 takes in one operand whole and an eighth of the other: the smaller one whole
+  const int experts_first = (long)a.E * (kWF32 ? 4 : 2) <= (long)a.T * 2;
   if (grid * 64 * kW > (long)UINT32_MAX) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((k_gate<kWF32, kM, kN, kW, kSW, kSX, kP>), dim3((unsigned)grid), dim3(64 * kW), 0, s, a, etiles, tiles);
+  hipLaunchKernelGGL((k_gate<kWF32, kE, kT, kW, kSW, kSX, kP>), dim3((unsigned)grid), dim3(64 * kW), 0, s, a, etiles, ttiles,
+                     experts_first);
   return hipGetLastError();
 }
 
-// The tile sizes built, in units of 16 experts and 16 tokens.  A workgroup fetches its rows of both
-// operands once, at 40 to 50 bytes a clock and compute unit whatever the tile, so the time goes as the bytes
-// of a tile's rows times the rounds its workgroups need on 256 compute units; the smallest product
-// wins, of equal ones the smaller tile.  Measured (BF16 weights, H 7168, E 256; us of the
-// chosen tile, next smaller, next larger): T 128 8.5, -, 10.5 (1 x 1); T 1024 13.4, 20.2, 17.8 (2 x 2); T 2048
-// 18.3, 25.2, 23.0 (4 x 2); T 4096 24.5, 34.6, 32.9 (4 x 4); T 8192 49.0, 63.4, - (8 x 4).
+// The tile sizes built (experts, tokens).  A workgroup fetches its rows of both operands once, at 40 to
+// 50 bytes a clock and compute unit whatever the tile, so the time goes as the bytes of a tile's rows
+// times the rounds its workgroups need on 256 compute units; the smallest product wins, of equal
+// ones the smaller tile.  Measured (us, H 7168, E 256; the chosen tile, the next smaller, the next larger):
+// BF16 weights T 1 5.1, -, 5.7; T 128 7.4, 10.9, 8.3 (8 x 16); T 1024 13.6, 20.5, 17.8 (32 x 32); T 2048 18.4,
+// 25.4, 23.2; T 4096 24.6, 34.9, 33.0; T 8192 49.6, 64.2, - (128 x 64); float32 weights T 1 6.7, -, 7.8; T 128
+// 9.9, 15.3, 10.7 (8 x 16); T 1024 20.7, 27.8, 25.3; T 8192 86.9, 120.3, - (64 x 128).
 struct Tile {
-  int m, n;
+  int e, t;
 };
-constexpr Tile kTilesBf16[] = {{1, 1}, {1, 2}, {2, 2}, {4, 2}, {4, 4}, {8, 4}};
-constexpr Tile kTilesF32[] = {{1, 1}, {1, 2}, {2, 2}, {2, 4}, {4, 8}};
+constexpr Tile kTilesBf16[] = {{8, 8}, {8, 16}, {16, 16}, {16, 32}, {32, 32}, {64, 32}, {64, 64}, {128, 64}};
+constexpr Tile kTilesF32[] = {{8, 8}, {8, 16}, {16, 16}, {16, 32}, {32, 32}, {32, 64}, {64, 128}};
 
 template <int kCount>
 int choose(const Tile (&tiles)[kCount], int weight_bytes, const GateArgs& a) {
@@ -278,8 +298,8 @@ int choose(const Tile (&tiles)[kCount], int weight_bytes, const GateArgs& a) {
   double least = 0;
   for (int i = 0; i < kCount; ++i) {
     const Tile t = tiles[i];
-    const long groups = (long)((a.E + 16 * t.m - 1) / (16 * t.m)) * (((long)a.T + 16 * t.n - 1) / (16 * t.n));
-    const double cost = (double)((groups + 255) / 256) * (t.m * weight_bytes + t.n * 2);
+    const long groups = (long)((a.E + t.e - 1) / t.e) * (((long)a.T + t.t - 1) / t.t);
+    const double cost = (double)((groups + 255) / 256) * (t.e * weight_bytes + t.t * 2);
     if (i == 0 || cost < least) best = i, least = cost;
   }
   return best;
@@ -290,20 +310,24 @@ int choose(const Tile (&tiles)[kCount], int weight_bytes, const GateArgs& a) {
 hipError_t launch_gate_logits(const GateArgs& a, hipStream_t s) {
   if (a.w_f32) {
     switch (choose(kTilesF32, 4, a)) {
-      case 0: return launch<true, 1, 1, 8, 2, 2, 1>(a, s);
-      case 1: return launch<true, 1, 2, 8, 2, 2, 1>(a, s);
-      case 2: return launch<true, 2, 2, 8, 1, 1, 2>(a, s);
-      case 3: return launch<true, 2, 4, 8, 1, 1, 2>(a, s);
-      default: return launch<true, 4, 8, 4, 1, 1, 4>(a, s);
+      case 0: return launch<true, 8, 8, 8, 6, 6, 1>(a, s);
+      case 1: return launch<true, 8, 16, 16, 2, 2, 1>(a, s);
+      case 2: return launch<true, 16, 16, 8, 2, 2, 1>(a, s);
+      case 3: return launch<true, 16, 32, 8, 2, 2, 1>(a, s);
+      case 4: return launch<true, 32, 32, 8, 1, 1, 2>(a, s);
+      case 5: return launch<true, 32, 64, 8, 1, 1, 2>(a, s);
+      default: return launch<true, 64, 128, 4, 1, 1, 4>(a, s);
     }
   }
   switch (choose(kTilesBf16, 2, a)) {
-    case 0: return launch<false, 1, 1, 8, 4, 4, 1>(a, s);
-    case 1: return launch<false, 1, 2, 8, 3, 3, 1>(a, s);
-    case 2: return launch<false, 2, 2, 8, 2, 2, 1>(a, s);
-    case 3: return launch<false, 4, 2, 8, 1, 2, 2>(a, s);
-    case 4: return launch<false, 4, 4, 8, 1, 1, 2>(a, s);
-    default: return launch<false, 8, 4, 4, 1, 2, 4>(a, s);
+    case 0: return launch<false, 8, 8, 8, 9, 9, 1>(a, s);
+    case 1: return launch<false, 8, 16, 8, 6, 6, 1>(a, s);
+    case 2: return launch<false, 16, 16, 8, 4, 4, 1>(a, s);
+    case 3: return launch<false, 16, 32, 8, 3, 3, 1>(a, s);
+    case 4: return launch<false, 32, 32, 8, 2, 2, 1>(a, s);
+    case 5: return launch<false, 64, 32, 8, 1, 2, 2>(a, s);
+    case 6: return launch<false, 64, 64, 8, 1, 1, 2>(a, s);
+    default: return launch<false, 128, 64, 4, 1, 2, 4>(a, s);
   }
 }
 

@@ -216,7 +216,8 @@ def _gate(x, w, stream=None):
 GATE_SHAPES = [(1, 128, 1), (1, 7168, 256), (2, 256, 7), (3, 1024, 60), (5, 7168, 256), (16, 2048, 64),
                (17, 384, 33), (31, 896, 130), (64, 4096, 128), (65, 640, 257), (100, 7168, 8), (128, 7168, 256),
                (200, 16384, 40), (257, 1280, 384), (513, 512, 160), (1021, 4096, 128), (1500, 256, 17),
-               (2050, 768, 256), (4099, 384, 192), (3, 256, 2051), (5000, 256, 200), (8197, 128, 131)]
+               (2050, 768, 256), (4099, 384, 192), (3, 256, 2051), (5000, 256, 200), (8197, 128, 131), (8, 640, 8),
+               (9, 1024, 9), (7, 128, 200), (130, 1152, 255), (40, 16384, 129)]
 
 
 @pytest.mark.parametrize("w", ["bf16", "f32"])
