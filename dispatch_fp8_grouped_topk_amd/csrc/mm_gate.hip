@@ -25,13 +25,13 @@ __device__ __forceinline__ int lower_part(int v) {
   return __builtin_bit_cast(int, __builtin_bit_cast(float, v) - __builtin_bit_cast(float, v & (int)0xFFFF0000));
 }
 
-// acc += w x for 8 float32 weights a lane (lo, hi) as three BF16 operands whose sum they are.
-__device__ __forceinline__ v4f mfma_split(v4i lo, v4i hi, const v4i& b, v4f acc) {
+// 8 float32 weights a lane as three BF16 operands whose sum they are.
+__device__ __forceinline__ void split3(const v4i (&w)[2], v4i (&parts)[3]) {
+  v4i lo = w[0], hi = w[1];
 #pragma unroll
   for (int term = 0; term < 3; ++term) {
-    const v4i t = {upper_halves(lo[0], lo[1]), upper_halves(lo[2], lo[3]), upper_halves(hi[0], hi[1]),
-                   upper_halves(hi[2], hi[3])};
-    acc = mfma_bf16(t, b, acc);
+    parts[term] = v4i{upper_halves(lo[0], lo[1]), upper_halves(lo[2], lo[3]), upper_halves(hi[0], hi[1]),
+                      upper_halves(hi[2], hi[3])};
     if (term == 2) break;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -39,7 +39,6 @@ __device__ __forceinline__ v4f mfma_split(v4i lo, v4i hi, const v4i& b, v4f acc)
       hi[i] = lower_part(hi[i]);
     }
   }
-  return acc;
 }
 
 // A 16-byte load of each lane from a buffer into consecutive LDS bytes from the wave-uniform `lds` on.
@@ -79,11 +78,13 @@ __global__ __launch_bounds__(64 * kW) void k_gate(GateArgs a, int etiles, int tt
   static_assert(kSX >= kSW && kM % kP == 0 && (kP == 1 || kP % 2 == 0), "");
   constexpr int kLater0 = kLW - kLP + (kSW - 1) * (kLX + kLW), kLater = kLater0 + kLX;
   static_assert(kLater < 64, "vmcnt holds 6 bits");
-  // A tile of 8 x 8 fills an MFMA with both halves of a step: rows and columns 0 .. 7 are its experts and tokens at
-  // columns 0 .. 31, rows and columns 8 .. 15 the same at columns 32 .. 63, and the sums of the two
-  // diagonal quarters are added at the end.
-  constexpr bool kFolded = kE == 8 && kT == 8;
-  constexpr int kSubs = kFolded ? 1 : 2;                 // MFMA steps of a step
+  // Eight experts fill an MFMA operand with both halves of a step: rows 0 .. 7 are its columns 0 .. 31, rows 8 .. 15 its
+  // columns 32 .. 63, read (and split) once.  Tokens are multiplied half by half into sums of their own, of
+  // which rows 0 .. 7 and rows 8 .. 15 count; or, eight of them, are folded the same way, one MFMA does
+  // both halves and the diagonal quarters count.  The two parts are added at the end.
+  constexpr bool kFoldE = kE == 8, kFoldT = kFoldE && kT == 8;
+  constexpr int kSubsW = kFoldE ? 1 : 2, kSubsX = kFoldT ? 1 : 2;
+  static_assert(!kFoldE || kT <= 16, "");
   constexpr int kXBytes = kLX * 1024, kWBytes = kLW * 1024;
   constexpr int kRing = kSX * kXBytes + kSW * kWBytes;   // a wave's LDS
   constexpr int kSums = kM * kN * 1024;                  // a wave's sums
@@ -119,7 +120,6 @@ __global__ __launch_bounds__(64 * kW) void k_gate(GateArgs a, int etiles, int tt
     const int r = rows == 8 ? col & 7 : col;
     return r * 128 + ((c ^ (r >> 1)) * 16);
   };
-  const auto half_at = [&](int s) { return kFolded ? col >> 3 : s; };
 
   const int all = a.H / 64, steps = all > wave ? (all - wave + kW - 1) / kW : 0;
   // Out of range is what lies at or past the buffer's size less the scalar offset, so the scalar offset
@@ -146,31 +146,32 @@ __global__ __launch_bounds__(64 * kW) void k_gate(GateArgs a, int etiles, int tt
     for (int n = 0; n < kLX; ++n) lds_load16(xr, xlane[n & 1] + out, k + rows_at(8 * n, trows, xstride), to + n * 1024);
   };
 
-  v4i X[2][kSubs][kN], W[2][kSubs][kMP][kHalves];
-  const auto read_x = [&](int slot, v4i (&to)[kSubs][kN]) {
+  v4i X[2][kSubsX][kN], W[2][kSubsW][kMP][kHalves];
+  const auto read_x = [&](int slot, v4i (&to)[kSubsX][kN]) {
     const char* xs = ring + slot * kXBytes;
 #pragma unroll
-    for (int s = 0; s < kSubs; ++s)
+    for (int s = 0; s < kSubsX; ++s)
 #pragma unroll
-      for (int n = 0; n < kN; ++n) to[s][n] = *reinterpret_cast<const v4i*>(xs + n * 2048 + chunk_at(4 * half_at(s) + lg, kT));
+      for (int n = 0; n < kN; ++n) to[s][n] = *reinterpret_cast<const v4i*>(xs + n * 2048 + chunk_at(4 * (kFoldT ? col >> 3 : s) + lg, kT));
   };
-  const auto read_w = [&](int slot, int p, v4i (&to)[kSubs][kMP][kHalves]) {
+  const auto read_w = [&](int slot, int p, v4i (&to)[kSubsW][kMP][kHalves]) {
     const char* ws = ring + kSX * kXBytes + slot * kWBytes + p * kLP * 1024;
 #pragma unroll
-    for (int s = 0; s < kSubs; ++s)
+    for (int s = 0; s < kSubsW; ++s)
 #pragma unroll
       for (int m = 0; m < kMP; ++m) {
+        const int half = kFoldE ? col >> 3 : s;
         if constexpr (kWF32) {
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            to[s][m][h] = *reinterpret_cast<const v4i*>(ws + (half_at(s) * kRows + 2 * m) * 1024 + chunk_at(2 * lg + h, kE));
+            to[s][m][h] = *reinterpret_cast<const v4i*>(ws + (half * kRows + 2 * m) * 1024 + chunk_at(2 * lg + h, kE));
         } else {
-          to[s][m][0] = *reinterpret_cast<const v4i*>(ws + m * 2048 + chunk_at(4 * half_at(s) + lg, kE));
+          to[s][m][0] = *reinterpret_cast<const v4i*>(ws + m * 2048 + chunk_at(4 * half + lg, kE));
         }
       }
   };
 
-  v4f acc[kM][kN];
+  v4f acc[kM][kN], acc_half = {0.f, 0.f, 0.f, 0.f};   // acc_half: a folded tile's second half of the columns
 #pragma unroll
   for (int m = 0; m < kM; ++m)
 #pragma unroll
@@ -212,16 +213,26 @@ __global__ __launch_bounds__(64 * kW) void k_gate(GateArgs a, int etiles, int tt
             read_w(sw1, 0, W[b ^ 1]);
           }
           __builtin_amdgcn_sched_barrier(0);
+          v4i parts[3];                            // float32 weights: the operand's terms
 #pragma unroll
-          for (int s = 0; s < kSubs; ++s)
+          for (int s = 0; s < kSubsX; ++s)
 #pragma unroll
-            for (int m = 0; m < kMP; ++m)
+            for (int m = 0; m < kMP; ++m) {
+              const v4i(&w)[kHalves] = W[b][kFoldE ? 0 : s][m];
+              if constexpr (kWF32) {
+                if (!kFoldE || s == 0) split3(w, parts);
+              }
 #pragma unroll
               for (int n = 0; n < kN; ++n) {
-                v4f& c = acc[p * kMP + m][n];
-                if constexpr (kWF32) c = mfma_split(W[b][s][m][0], W[b][s][m][1], X[u][s][n], c);
-                else c = mfma_bf16(W[b][s][m][0], X[u][s][n], c);
+                v4f& c = kFoldE && s == 1 ? acc_half : acc[p * kMP + m][n];
+                if constexpr (kWF32) {
+#pragma unroll
+                  for (int term = 0; term < 3; ++term) c = mfma_bf16(parts[term], X[u][s][n], c);
+                } else {
+                  c = mfma_bf16(w[0], X[u][s][n], c);
+                }
               }
+            }
           __builtin_amdgcn_sched_barrier(0);
           asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // read: the place may be filled again
           if (p + 1 < kP) {
@@ -243,15 +254,16 @@ __global__ __launch_bounds__(64 * kW) void k_gate(GateArgs a, int etiles, int tt
 #pragma unroll
   for (int m = 0; m < kM; ++m)
 #pragma unroll
-    for (int n = 0; n < kN; ++n) sums[(wave * kM * kN + m * kN + n) * 64 + lane] = acc[m][n];
+    for (int n = 0; n < kN; ++n)
+      sums[(wave * kM * kN + m * kN + n) * 64 + lane] = kFoldE && !kFoldT && lg >= 2 ? acc_half : acc[m][n];
   __syncthreads();
   for (int j = wave; j < kM * kN; j += kW) {
     v4f sum = sums[j * 64 + lane];
 #pragma unroll
     for (int w = 1; w < kW; ++w) sum += sums[(w * kM * kN + j) * 64 + lane];
-    if constexpr (kFolded) {                       // the lane of row + 8, column + 8
+    if constexpr (kFoldE) {                        // the lane of row + 8 and, folded, column + 8
 #pragma unroll
-      for (int w = 0; w < kW; ++w) sum += sums[w * 64 + ((lane + 40) & 63)];
+      for (int w = 0; w < kW; ++w) sum += sums[w * 64 + ((lane + (kFoldT ? 40 : 32)) & 63)];
     }
     const int e = e0 + 16 * (j / kN) + 4 * lg;
     const long t = t0 + 16 * (j % kN) + col;
