@@ -126,8 +126,14 @@ __global__ __launch_bounds__(64 * kW) void k_gate(GateArgs a, int etiles, int tt
   // itself stays inside: loads of a step past the last one, which count but fetch nothing, get a lane
   // offset of 2^31 and scalar offset 0, and loads of eight rows that are all past the tile's last
   // take the first eight.
+  // The XCDs start at different columns and wrap round, so that they do not all ask for the same columns of
+  // their rows at once (2 to 4% at T 1024 to 8192).
+  const int turn = (int)(blockIdx.x & 7) * steps >> 3;
   const auto beyond = [&](int i) { return i < steps ? 0u : 0x80000000u; };
-  const auto column = [&](int i) { return i < steps ? (uint32_t)(wave + kW * i) : 0u; };
+  const auto column = [&](int i) {
+    const int j = i + turn;
+    return i < steps ? (uint32_t)(wave + kW * (j < steps ? j : j - steps)) : 0u;
+  };
   const auto rows_at = [&](int r, int rows, uint32_t stride) { return r < rows ? (uint32_t)r * stride : 0u; };
   const auto fetch_w = [&](int i, int slot, int p) {
     const uint32_t k = column(i) * (128 * kHalves), out = beyond(i);
