@@ -527,15 +527,19 @@ MM_EXPORT int mega_moe_gate_logits(const mega_moe_gate_problem* p, const void* x
   const int st = check_device();
   if (st) return st;
   mm::GateArgs a{};
-  a.x = static_cast<const uint16_t*>(x);
   a.w = w;
-  a.logits = logits;
   a.x_stride = xs;
-  a.T = (int)T;
   a.H = (int)H;
   a.E = (int)E;
   a.w_f32 = p->weight_dtype == MEGA_MOE_DTYPE_F32;
-  return mm::launch_gate_logits(a, static_cast<hipStream_t>(stream)) == hipSuccess ? MEGA_MOE_OK : MEGA_MOE_ERR_HIP;
+  // a launch holds fewer than 2^32 threads: 2^23 tokens of any number of experts
+  for (int64_t t = 0; t < T; t += mm::kGateTokens) {
+    a.x = static_cast<const uint16_t*>(x) + (size_t)t * xs;
+    a.logits = logits + (size_t)t * E;
+    a.T = (int)std::min<int64_t>(T - t, mm::kGateTokens);
+    if (mm::launch_gate_logits(a, static_cast<hipStream_t>(stream)) != hipSuccess) return MEGA_MOE_ERR_HIP;
+  }
+  return MEGA_MOE_OK;
 }
 
 MM_EXPORT int mega_moe_gate_topk(const mega_moe_topk_problem* p, const void* logits, const float* bias,

@@ -7,6 +7,7 @@
 namespace mm {
 
 constexpr int kMaxGroups = 64;        // expert groups: one lane of a wave each
+constexpr int64_t kGateTokens = 1 << 23;   // tokens of one launch of the gate product
 constexpr long kMaxGateStride = 1 << 22;  // the gate addresses a tile's rows of x with 31-bit offsets
 
 struct NormArgs {

@@ -302,7 +302,8 @@ int mega_moe_diag_mfma_block_sums(int fmt, const void* a, const void* b, const v
  *
  * They need no workspace, allocate and synchronise nothing, keep nothing between calls and can be
  * captured into a HIP graph; each is one kernel launch on `stream` (a hipStream_t, NULL for the
- * default stream), whose device has to be the current one.  Pointers are device memory, 16-byte
+ * default stream; the gate product: one for every 2^23 tokens), whose device has to be the current
+ * one.  Pointers are device memory, 16-byte
  * aligned unless stated.  Arguments are validated synchronously, before the device is touched;
  * num_tokens == 0 is a valid no-op.  An output overlaps no input and no other output, from its
  * first element to its last, except where stated (INVALID_ARG).  Results are repeatable bit for bit.  Errors: INVALID_ARG, NULL_POINTER,

@@ -252,6 +252,19 @@ def test_gate_float32_weights_keep_all_their_bits():
         assert torch.equal(_gate(x[:rows].contiguous(), W), W.t()[:rows])
 
 
+@pytest.mark.parametrize("E", [1, 9])
+def test_gate_logits_of_more_tokens_than_one_launch_takes(E):
+    T, H = (1 << 23) + 77, 128
+    x = torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")
+    rows = torch.tensor([0, 1, 4095, (1 << 23) - 1, 1 << 23, (1 << 23) + 63, T - 1], device="cuda")
+    x[rows] = torch.randint(-4, 5, (len(rows), H), generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    W = torch.randint(-8, 9, (E, H), generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).cuda()
+    logits = _gate(x, W)
+    assert torch.equal(logits[rows], (x[rows].float().cpu() @ W.float().cpu().t()).cuda())
+    logits[rows] = 0
+    assert not logits.any()
+
+
 @pytest.mark.parametrize("T", [1, 40, 700])
 @pytest.mark.parametrize("w", ["bf16", "f32"])
 def test_gate_values_that_are_not_finite_stay_in_their_row(T, w):
