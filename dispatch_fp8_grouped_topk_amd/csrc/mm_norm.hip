@@ -176,7 +176,7 @@ __global__ __launch_bounds__(1024) void k_norm_quant(NormArgs a) {
         const float inv = 448.0f / amax;
         out.x = e4m3_scaled4(v[0], v[1], v[2], v[3], inv, sf);
         out.y = e4m3_scaled4(v[4], v[5], v[6], v[7], inv, sf);
-        if (m == 0) out = make_uint2(0, 0);
+        if (sf == 0.f) out = make_uint2(0, 0);       // all zero, or below float32's range
         if (m >= kInfBits) out = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
         if ((tid & 15) == 0) static_cast<float*>(a.q_sf)[(size_t)row * (a.H / 128) + c / 16] = sf;
       } else {

@@ -148,8 +148,8 @@ __global__ __launch_bounds__(64) void k_topk_lds(TopkArgs a) {
   }
 }
 
-// exp(x) in float64 to about an ulp, for any x (NaN excepted): x = n ln 2 + r with |r| <= ln 2 / 2, the
-// Taylor series of exp(r) to r^13 / 13! (the next term is below 2^-57), times 2^n.
+// exp(x) in float64 to about an ulp, for any x (NaN excepted): x = n ln 2 + r with |r| <= ln 2 / 2 (Cody and
+// Waite's reduction), the Taylor series of exp(r) to r^13 / 13! (the next term is below 2^-57), times 2^n.
 __device__ __forceinline__ double exp64(double x) {
   x = fmin(fmax(x, -800.0), 800.0);              // 2^n is 0 or infinity there
   const double n = __builtin_rint(x * 1.4426950408889634);
@@ -311,7 +311,7 @@ __device__ __forceinline__ void load_bias(const TopkArgs& a, int e0, int mine, b
   for (int j = 0; j < kN; ++j) b[j] = cleaned(b[j]);
 }
 
-// A chosen expert's weight before the renormalisation, 0 where there is none: in float32 (to 2^-20) unless one
+// A chosen expert's weight before the renormalisation, 0 where there is none: in float32 (to 2^-18) unless one
 // of the row's is so small that float32's range or the renormalisation's 1e-20 would matter.
 template <class Score32, class Score64>
 __device__ __forceinline__ double weight_of(bool has, float logit, const Score32& score32, const Score64& score64) {
@@ -322,9 +322,14 @@ __device__ __forceinline__ double weight_of(bool has, float logit, const Score32
 
 // Whether two float32 ordering values may be out of order (see k_topk_wave).
 struct Close {
-  float step;                                    // for scores: below twice their error
+  float step;                                    // at least twice the error of a score
   __device__ __forceinline__ bool operator()(float u, float v) const {
     return !(fabsf(u - v) > step + 0x1p-22f * fmaxf(fabsf(u), fabsf(v)));       // also where it is NaN
+  }
+  // The same for groups' values, sums of two; mu, mv: the sums of their terms' magnitudes, which the
+  // terms' roundings go by.
+  __device__ __forceinline__ bool groups(float u, float v, float mu, float mv) const {
+    return !(fabsf(u - v) > 2.f * step + 0x1p-21f * fmaxf(mu, mv));
   }
   static __device__ __forceinline__ Close of(bool sigmoid, float largest) { return {sigmoid ? 0x1p-20f : largest * 0x1p-16f}; }
 };
@@ -485,10 +490,14 @@ __global__ __launch_bounds__(256) void k_topk_wave(TopkArgs a, int log2_lanes, i
     const Close close = Close::of(a.sigmoid, unit);
     if (a.G > 1) {
       best_two(m1, m2, log2_lanes);
-      float v = m1;
+      float v = m1, size = fabsf(m1);            // size: the magnitudes of what v is the sum of
       if (a.group_top == 2 && m1 > -kInf32) {
-        if constexpr (kBiased) v = m2 > -kInf32 ? m1 + m2 : m1;
-        else v = score32(m1) + (m2 > -kInf32 ? score32(m2) : 0.f);
+        if constexpr (kBiased) {
+          v = m2 > -kInf32 ? m1 + m2 : m1;
+          size = m2 > -kInf32 ? fabsf(m1) + fabsf(m2) : fabsf(m1);
+        } else {
+          size = v = score32(m1) + (m2 > -kInf32 ? score32(m2) : 0.f);
+        }
       }
       int rank = 0;                              // groups that come before this lane's
       for (int o = 0; o < a.G; ++o) {
@@ -496,13 +505,14 @@ __global__ __launch_bounds__(256) void k_topk_wave(TopkArgs a, int log2_lanes, i
         rank += u > v || (u == v && o < g);
       }
       if (by_score) {
-        // the last group kept and the first one dropped, each a sum of two: half the distance counts
+        // the last group kept and the first one dropped
         const int last = __builtin_ctzll(__ballot(rank == a.KG - 1) | 1ull << 63);
         const uint64_t out = __ballot(rank == a.KG && g < a.G);
         if (out) {
-          const float u = __uint_as_float(lane_value(__float_as_uint(v), last));
-          const float d = __uint_as_float(lane_value(__float_as_uint(v), __builtin_ctzll(out)));
-          if (d > -kInf32 && close(0.5f * u, 0.5f * d)) {
+          const int first = __builtin_ctzll(out);
+          const auto at_lane = [](float f, int from) { return __uint_as_float(lane_value(__float_as_uint(f), from)); };
+          const float d = at_lane(v, first);
+          if (d > -kInf32 && close.groups(at_lane(v, last), d, at_lane(size, last), at_lane(size, first))) {
             uint32_t hi[kN], lo[kN];
             need_total();
             rank = order64(a, at, l, b, score64, hi, lo);
@@ -726,10 +736,14 @@ __global__ __launch_bounds__(256) void k_topk_quarter(TopkArgs a, int log2_lanes
     const Close close = Close::of(a.sigmoid, unit);
     if (a.G > 1) {
       best_two(m1, m2, log2_lanes);
-      float v = m1;
+      float v = m1, size = fabsf(m1);            // size: the magnitudes of what v is the sum of
       if (a.group_top == 2 && m1 > -kInf32) {
-        if constexpr (kBiased) v = m2 > -kInf32 ? m1 + m2 : m1;
-        else v = score32(m1) + (m2 > -kInf32 ? score32(m2) : 0.f);
+        if constexpr (kBiased) {
+          v = m2 > -kInf32 ? m1 + m2 : m1;
+          size = m2 > -kInf32 ? fabsf(m1) + fabsf(m2) : fabsf(m1);
+        } else {
+          size = v = score32(m1) + (m2 > -kInf32 ? score32(m2) : 0.f);
+        }
       }
       if (g >= a.G) v = -kInf32;
       int before = 0;                            // lanes of the groups that come before this lane's
@@ -740,9 +754,13 @@ __global__ __launch_bounds__(256) void k_topk_quarter(TopkArgs a, int log2_lanes
       });
       bool kept = before < a.KG << log2_lanes;
       if (by_score) {
-        // the last group kept and the first one dropped, each a sum of two: half the distance counts
-        const uint32_t least = row_max(kept ? ~key32(v) : 0u), most = row_max(kept || v == -kInf32 ? 0u : key32(v));
-        const uint64_t which = __ballot(row < valid && most != 0 && close(0.5f * value32(~least), 0.5f * value32(most)));
+        // the last group kept and the first one dropped
+        const float last = value32(~row_max(kept ? ~key32(v) : 0u));
+        const uint32_t most = row_max(kept || v == -kInf32 ? 0u : key32(v));
+        const float first = value32(most);
+        // (sizes are not negative: their bits order as they do)
+        const float sizes = __uint_as_float(row_max(v == last || v == first ? __float_as_uint(size) : 0u));
+        const uint64_t which = __ballot(row < valid && most != 0 && close.groups(last, first, sizes, sizes));
         if (which) {
           for (int q = 0; q < 4; ++q) {
             if (!((which >> (16 * q)) & 0xFFFF)) continue;

@@ -332,7 +332,8 @@ typedef struct {
  *   q, q_sf = v in 8 bits as the forward's x, x_sf of the recipe: per group of 128 columns
  *     q_sf = amax/448 (float32), q = E4M3(v / q_sf); or per group of 32 the UE8M0 code of the
  *     smallest power of two s with amax/s <= 448 (at least 2^-127; decided as if in float64), and
- *     q = E4M3(v / s).  An all-zero group has scale 0 (code 0) and codes 0.
+ *     q = E4M3(v / s).  A group whose scale is 0 (code 0 for one that is
+ *     all zero) has codes 0.
  * A row with a value that is not finite (in h) has NaN normed, q and q_sf (E4M3 0x7F or 0xFF, UE8M0
  * code 255), a group with a v that is not finite has NaN q and q_sf; other rows and groups are
  * not affected.

@@ -193,6 +193,35 @@ def test_norm_zeros_infinities_and_large_values(recipe):
     assert torch.equal(got2["q_sf"][0][keep], got["q_sf"][0][keep])
 
 
+def test_norm_values_below_float32s_normal_numbers():
+    X = torch.randn(3, 256, generator=torch.Generator().manual_seed(8)).cuda()
+    X[:, 5] = 0
+    for size in (1e-38, 1e-41, 1e-44, 0.0):
+        W = torch.full((256,), size, device="cuda")
+        got = _norm(X, None, W, 0)
+        q = E4M3[got["q"].cpu().numpy()]
+        assert np.isfinite(q).all() and (q[:, 5] == 0).all() and torch.isfinite(got["q_sf"]).all()
+        assert (got["q"].view(3, 2, 128)[got["q_sf"] == 0] == 0).all()
+        got = _norm(X, None, W, 1)
+        assert np.isfinite(E4M3[got["q"].cpu().numpy()]).all()
+        # half a code's step at the smallest scale, and what the values themselves have lost
+        v = _f64(X) / np.sqrt((_f64(X) ** 2).mean(axis=1, keepdims=True) + 1e-6) * _f64(W)
+        scale = np.ldexp(1.0, np.repeat(got["q_sf"].cpu().numpy().astype(int), 32, axis=1) - 127)
+        err = np.abs(E4M3[got["q"].cpu().numpy()] * scale - v)
+        assert (err <= np.abs(v) * 2.0 ** -4 * 1.01 + 2.0 ** -10 * scale + 2.0 ** -148).all()
+
+
+def test_norm_more_rows_than_workgroups():
+    T = (1 << 20) + 3
+    X = torch.ones(T, 128, dtype=torch.bfloat16, device="cuda")
+    X[1 << 20:] = torch.randn(3, 128, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    W = torch.ones(128, dtype=torch.bfloat16, device="cuda")
+    got = _norm(X, None, W, 1)
+    tail = slice(T - 5, T)
+    _check_norm({k: None if v is None else v[tail] for k, v in got.items()}, X[tail], None, W, 1)
+    assert (got["normed"][:1 << 20] == got["normed"][0, 0]).all() and (got["q_sf"][:1 << 20] == got["q_sf"][0, 0]).all()
+
+
 def test_norm_no_tokens():
     for recipe in (0, 1):
         _norm(torch.empty(0, 256, dtype=torch.bfloat16, device="cuda"), None,
@@ -417,6 +446,19 @@ def test_topk_scores_a_rounding_apart(E, times, G, KG, group_top, biased, score)
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("size", [2.0 ** 20, 3.0e37])
+@pytest.mark.parametrize("times", [1, 21])
+def test_topk_group_sums_whose_terms_cancel(times, size, score):
+    """Two experts a group with biases of opposite sign: the sums are of the order of the scores while their
+    terms round by far more."""
+    g = torch.Generator().manual_seed(15)
+    logits = torch.randn(200, 64, generator=g)
+    bias = torch.full((64,), -float("inf"))
+    bias[0::8], bias[3::8] = size, -size
+    _check_topk(logits.cuda(), 6, bias.cuda(), times=times, score=score, num_groups=8, topk_groups=4, group_top=2)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("G,KG,group_top", [(1, 1, 1), (4, 2, 1), (4, 2, 2)])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("E,times", [(32, 1), (32, 342), (256, 1), (256, 683), (1024, 1)])
@@ -443,6 +485,21 @@ def test_topk_masked_experts(E, times, dtype, G, KG, group_top, score):
         for renorm in (False, True):
             _check_topk(logits, k, b, times=times, score=score, num_groups=G, topk_groups=KG, group_top=group_top,
                         renorm=renorm, num_shared=1)
+
+
+@pytest.mark.parametrize("T,E,k,dtype", [((1 << 24) + 5, 2, 1, "f32"), ((1 << 22) + 5, 16, 15, "bf16"),
+                                         ((1 << 20) + 3, 520, 2, "bf16")])
+def test_topk_more_rows_than_one_pass_of_the_workgroups(T, E, k, dtype):
+    logits = torch.zeros(T, E, dtype=DT[dtype][1], device="cuda")
+    logits[:, E - 1] = 1                                      # the last expert, then from the first on
+    tail = torch.randn(9, E, generator=torch.Generator().manual_seed(3)).to(DT[dtype][1]).cuda()
+    logits[T - 9:] = tail
+    idx, w = _topk(logits, k, renorm=True)
+    ref_i, ref_w = front.gate_topk(_f64(tail), None, k, renorm=True)
+    assert np.array_equal(idx[T - 9:].cpu().numpy(), ref_i)
+    assert (np.abs(_f64(w[T - 9:]) - ref_w) <= 2.0 ** -18 * ref_w).all()
+    first = torch.tensor([E - 1, *range(k - 1)], dtype=torch.int32, device="cuda")
+    assert (idx[:T - 9] == first).all() and (w[:T - 9] == w[0]).all()
 
 
 @pytest.mark.parametrize("n", [-3, 0, 1, 30, 37, 100])
