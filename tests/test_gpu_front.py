@@ -274,7 +274,8 @@ def test_gate_logits_whole_numbers_are_exact(T, H, E, w):
 def test_gate_float32_weights_keep_all_their_bits():
     g = torch.Generator().manual_seed(5)
     T = H = 256
-    W = torch.randn(31, H, generator=g).cuda() * torch.exp2(torch.randint(-60, 60, (31, H), generator=g).float()).cuda()
+    W = (1 + torch.rand(31, H, generator=g)) * torch.exp2(torch.randint(-102, 100, (31, H), generator=g).float())
+    W = torch.where(torch.rand(31, H, generator=g) < 0.5, W, -W).cuda()
     x = torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")
     x[torch.arange(T), torch.arange(T)] = 1.0
     for rows in (T, 3):
