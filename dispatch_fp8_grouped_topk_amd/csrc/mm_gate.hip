@@ -3,7 +3,7 @@
 // Weights are the MFMA's A operand (rows are experts) and tokens its B operand (columns), so a lane
 // ends with four consecutive experts of one token.  Float32 weights are split into three BF16 terms of
 // 8 significant bits each (w = hi + mid + lo exactly, by truncation) and multiplied by three MFMAs
-// into the same sum.
+// into the same sum.  A few logits are dot products of rows instead, with float32 multiply-adds (k_gate_rows).
 #include "mm_front.h"
 
 namespace mm {
@@ -303,13 +303,82 @@ hipError_t launch(const GateArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Products of few tokens: a workgroup for an expert and kT tokens, its lanes along their rows, straight
+// from memory to registers, 8192 columns in flight at once, so that a row is one memory latency; the
+// sums of 256 lanes are joined at the end.  Every term is one float32 multiply-add with the weight as it
+// stands (float32 too), rounded once.  What bounds it is that latency and, with more tokens, the rows read
+// again from L2.
+template <bool kWF32, int kT>
+__global__ __launch_bounds__(256) void k_gate_rows(GateArgs a) {
+  constexpr int kB = 4, kWL = kWF32 ? 2 : 1;
+  __shared__ float part[kT][4];
+  const int tid = threadIdx.x, chunks = a.H / 8, e = blockIdx.x, t0 = blockIdx.y * kT;
+  const v4i* wrow = reinterpret_cast<const v4i*>(static_cast<const char*>(a.w) + (size_t)e * a.H * (kWF32 ? 4 : 2));
+  float acc[kT] = {};
+  for (int c0 = 0; c0 < chunks; c0 += 256 * kB) {
+    v4i w[kB][kWL], x[kB][kT];
+#pragma unroll
+    for (int b = 0; b < kB; ++b) {
+      const int c = c0 + 256 * b + tid;
+#pragma unroll
+      for (int l = 0; l < kWL; ++l) w[b][l] = v4i{0, 0, 0, 0};
+#pragma unroll
+      for (int t = 0; t < kT; ++t) x[b][t] = v4i{0, 0, 0, 0};
+      if (c < chunks) {
+#pragma unroll
+        for (int l = 0; l < kWL; ++l) w[b][l] = wrow[c * kWL + l];
+#pragma unroll
+        for (int t = 0; t < kT; ++t)
+          x[b][t] = reinterpret_cast<const v4i*>(a.x + (size_t)min(t0 + t, a.T - 1) * a.x_stride)[c];
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < kB; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int p = w[b][0][i];                  // BF16 weights: a pair
+        const int lo = kWF32 ? w[b][i / 2 * (kWL - 1)][2 * (i % 2)] : p << 16;
+        const int hi = kWF32 ? w[b][i / 2 * (kWL - 1)][2 * (i % 2) + 1] : p & (int)0xFFFF0000;
+#pragma unroll
+        for (int t = 0; t < kT; ++t) {
+          const int u = x[b][t][i];
+          acc[t] = __builtin_fmaf(__int_as_float(lo), __int_as_float(u << 16), acc[t]);
+          acc[t] = __builtin_fmaf(__int_as_float(hi), __int_as_float(u & (int)0xFFFF0000), acc[t]);
+        }
+      }
+  }
+#pragma unroll
+  for (int t = 0; t < kT; ++t) {
+    const float sum = wave_sum63(acc[t]);
+    if (tid % 64 == 63) part[t][tid / 64] = sum;
+  }
+  __syncthreads();
+  if (tid < kT && t0 + tid < a.T)
+    a.logits[(size_t)(t0 + tid) * a.E + e] = part[tid][0] + part[tid][1] + part[tid][2] + part[tid][3];
+}
+
+template <bool kWF32, int kT>
+hipError_t launch_rows(const GateArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((k_gate_rows<kWF32, kT>), dim3(a.E, (a.T + kT - 1) / kT), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+// Rows of a few tokens go to k_gate_rows as long as reading them again for each logit costs less than the
+// tiles' K loop of fixed length.  Measured (us, rows with one token a workgroup, with two, tiles; H 7168, E 256):
+// BF16 weights T 1 2.4, 2.7, 5.1; T 4 3.0, 3.0, 5.1; T 8 3.8, 3.7, 5.1; T 16 5.5, 4.9, 5.1; float32 T 1 2.5,
+// 2.7, 6.9; T 4 3.4, 3.3, 7.0; T 8 4.6, 4.2, 6.9; T 16 7.5, 6.1, 6.9.  T 32, E 64, H 4096 3.5, 3.4, 4.4; with few
+// experts the tiles win sooner: T 256, E 8, H 7168 6.3, 6.4, 5.0.
+constexpr int kRowsTokens = 64;
+constexpr long kRowsLogits = 2048;
+constexpr int kRowsSingle = 512;
+
 // The tile sizes built (experts, tokens).  A workgroup fetches its rows of both operands once, at 40 to
 // 50 bytes a clock and compute unit whatever the tile, so the time goes as the bytes of a tile's rows
 // times the rounds its workgroups need on 256 compute units; the smallest product wins, of equal
 // ones the smaller tile.  Measured (us, H 7168, E 256; the chosen tile, the next smaller, the next larger):
-// BF16 weights T 1 5.1, -, 5.7; T 128 7.4, 10.9, 8.3 (8 x 16); T 1024 13.6, 20.5, 17.8 (32 x 32); T 2048 18.4,
-// 25.4, 23.2; T 4096 24.6, 34.9, 33.0; T 8192 49.6, 64.2, - (128 x 64); float32 weights T 1 6.7, -, 7.8; T 128
-// 9.9, 15.3, 10.7 (8 x 16); T 1024 20.7, 27.8, 25.3; T 8192 86.9, 120.3, - (64 x 128).
+// BF16 weights T 1 (without k_gate_rows) 5.1, -, 5.7; T 128 7.4, 10.9, 8.3 (8 x 16); T 1024 13.6, 20.5, 17.8 (32 x 32); T 2048 18.4,
+// 25.4, 23.2; T 4096 24.6, 34.9, 33.0; T 8192 49.6, 64.2, - (128 x 64); float32 weights T 1 6.7, -, 7.8;
+// T 128 // 9.9, 15.3, 10.7 (8 x 16); T 1024 20.7, 27.8, 25.3; T 8192 86.9, 120.3, - (64 x 128).
 struct Tile {
   int e, t;
 };
@@ -332,6 +401,10 @@ int choose(const Tile (&tiles)[kCount], int weight_bytes, const GateArgs& a) {
 }  // namespace
 
 hipError_t launch_gate_logits(const GateArgs& a, hipStream_t s) {
+  if (a.T <= kRowsTokens && (long)a.T * a.E <= kRowsLogits) {
+    if (a.T == 1 || a.T * a.E <= kRowsSingle) return a.w_f32 ? launch_rows<true, 1>(a, s) : launch_rows<false, 1>(a, s);
+    return a.w_f32 ? launch_rows<true, 2>(a, s) : launch_rows<false, 2>(a, s);
+  }
   if (a.w_f32) {
     switch (choose(kTilesF32, 4, a)) {
       case 0: return launch<true, 8, 8, 8, 6, 6, 1>(a, s);

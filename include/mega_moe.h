@@ -361,9 +361,10 @@ typedef struct {
 
 /* Gate product: logits[t, e] = sum_h x[t, h] * w[e, h], products exact, sums in float32.
  *   x bf16 [T, H], rows x_stride apart;  w [E, H] weight_dtype;  logits f32 [T, E]
- * Float32 weights are multiplied as the sum of three BF16 terms, which hold every float32 of
- * magnitude 2^-102 or more exactly; with them an infinity in x or w gives NaN.  A value that is not
- * finite affects only the logits of its row of x or of its expert. */
+ * Float32 weights are multiplied as they stand where there are few logits, otherwise as the sum of three
+ * BF16 terms, which hold every float32 of magnitude 2^-102 or more exactly; with them an infinity in x or
+ * w gives an infinity or NaN.  A value that is not finite affects only the logits of its row of x or of
+ * its expert. */
 int mega_moe_gate_logits(const mega_moe_gate_problem* p, const void* x, const void* w, float* logits,
                          void* stream);
 

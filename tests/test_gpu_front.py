@@ -282,6 +282,59 @@ def test_gate_float32_weights_keep_all_their_bits():
         assert torch.equal(_gate(x[:rows].contiguous(), W), W.t()[:rows])
 
 
+# both sides of the sizes at which few logits are taken as dot products of rows: 64 tokens, 2048 logits, one
+# or two tokens a workgroup (512 logits), rows of one pass of 8192 columns and of more
+GATE_EDGES = [(64, 512, 32), (65, 512, 31), (64, 384, 33), (1, 256, 2048), (1, 256, 2049), (2, 640, 256),
+              (2, 640, 257), (2, 512, 1024), (2, 512, 1025), (3, 8192, 255), (3, 8320, 171), (7, 16384, 256),
+              (1, 16384, 3), (5, 128, 1), (63, 8064, 1), (33, 1152, 62), (33, 1152, 63)]
+
+
+@pytest.mark.parametrize("w", ["bf16", "f32"])
+@pytest.mark.parametrize("T,H,E", GATE_EDGES)
+def test_gate_logits_of_few_rows(T, H, E, w):
+    """Each term (three of them with weights in three parts) is added to a sum that the terms' magnitudes
+    bound, with an error of at most a step of it, 2^-23 (matrix instructions need not round to nearest); a few
+    more additions join the parts."""
+    _say("gate rows", T, H, E, w)
+    g = torch.Generator().manual_seed(T * 11 + E)
+    x = _rows(torch.randn(T, H, generator=g).to(torch.bfloat16).cuda(), 8 * (T % 4))
+    W = (torch.randn(E, H, generator=g) * 0.02).to(DT[w][1]).cuda()
+    got = _f64(_gate(x, W))
+    ref, mag = front.gate_logits(_f64(x), _f64(W))
+    assert (np.abs(got - ref) <= (H * (3 if w == "f32" else 1) + 8) * 2.0 ** -23 * mag).all()
+    xi = torch.randint(-4, 5, (T, H), generator=g).to(torch.bfloat16).cuda()
+    Wi = torch.randint(-8, 9, (E, H), generator=g).to(DT[w][1]).cuda()
+    assert torch.equal(_gate(xi, Wi).double(), (xi.cpu().double() @ Wi.cpu().double().t()).cuda())
+
+
+@pytest.mark.parametrize("w", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 3, 6, 700])
+def test_gate_infinities_give_no_finite_logits(T, w):
+    g = torch.Generator().manual_seed(8)
+    x = (1 + torch.rand(T, 640, generator=g)).to(torch.bfloat16).cuda()
+    W = (1 + torch.rand(50, 640, generator=g)).to(DT[w][1]).cuda()
+    clean = _gate(x, W).clone()
+    x[T - 1, 639] = float("inf")
+    W[49, 5] = -float("inf")
+    got = _gate(x, W)
+    assert not torch.isfinite(got[T - 1]).any() and not torch.isfinite(got[:, 49]).any()
+    assert torch.isnan(got[T - 1, 49])
+    assert torch.equal(got[:T - 1, :49], clean[:T - 1, :49])
+
+
+@pytest.mark.parametrize("w", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 4])
+def test_gate_weights_below_the_normal_range_of_few_rows(T, w):
+    """One term a logit, x = 1: the weight itself, subnormal or not."""
+    e = torch.arange(-140 if w == "f32" else -133, -100)
+    W = torch.zeros(len(e), 128)
+    W[torch.arange(len(e)), torch.arange(len(e)) % 128] = torch.exp2(e.double()).float()
+    assert (W.sum(1) > 0).all()
+    x = torch.ones(T, 128, dtype=torch.bfloat16, device="cuda")
+    got = _gate(x, W.to(DT[w][1]).cuda())
+    assert torch.equal(got, W.sum(1).cuda().expand(T, -1))
+
+
 @pytest.mark.parametrize("E", [1, 9])
 def test_gate_logits_of_more_tokens_than_one_launch_takes(E):
     T, H = (1 << 23) + 77, 128
