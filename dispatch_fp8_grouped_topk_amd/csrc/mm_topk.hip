@@ -326,12 +326,22 @@ struct Close {
   __device__ __forceinline__ bool operator()(float u, float v) const {
     return !(fabsf(u - v) > step + 0x1p-22f * fmaxf(fabsf(u), fabsf(v)));       // also where it is NaN
   }
-  // The same for groups' values, sums of two; mu, mv: the sums of their terms' magnitudes, which the
-  // terms' roundings go by.
-  __device__ __forceinline__ bool groups(float u, float v, float mu, float mv) const {
-    return !(fabsf(u - v) > 2.f * step + 0x1p-21f * fmaxf(mu, mv));
-  }
+  // How far a group's value, a sum of up to two biased scores, may be off, with as much again of what it rounds by:
+  // two scores' errors, and 2^-23 of the biased scores' magnitudes, whose sum is `size`.
+  __device__ __forceinline__ float of_group(float size) const { return step + 0x1p-22f * size; }
   static __device__ __forceinline__ Close of(bool sigmoid, float largest) { return {sigmoid ? 0x1p-20f : largest * 0x1p-16f}; }
+};
+
+// What a group's value lies between, as keys (0 where the group has no candidate).  The groups kept are the right
+// ones if each one's lower end is above every dropped one's upper end.  Every group counts, not the two at the border
+// alone: one whose two terms are large and cancel is off by their roundings wherever its sum stands in the order.
+struct Ends {
+  uint32_t lower, upper;
+  __device__ __forceinline__ Ends(float v, float size, const Close& close) {
+    const float off = close.of_group(size);      // an infinite size (an infinite bias, an overflow) leaves nothing sure
+    lower = v == -kInf32 ? 0u : key32(off < kInf32 ? v - off : -kInf32);
+    upper = v == -kInf32 ? 0u : key32(off < kInf32 ? v + off : kInf32);
+  }
 };
 
 // One row's ordering values in float64: as keys (0: cannot be chosen), and the number of groups that come
@@ -413,10 +423,10 @@ __device__ __forceinline__ int choose64(const TopkArgs& a, const Spread& at, con
 // of up to 1024 exponentials), the sum with the bias rounds by 2^-24 of itself.  Values further apart than
 // at least twice these errors (Close) are in the right order.  So k + 2 experts are taken: where neighbours
 // among the first k + 1 are close, those are ordered again by their float64 values, one a lane; where
-// the k-th, k + 1-st and k + 2-nd are close to one another, or the last group kept and the first one dropped,
-// the whole row is decided again in float64 (choose64).  On random rows of 256 experts the former
-// is one row in several hundred, the latter one in ten thousand.  Without a bias the logits are
-// compared, which is exact.
+// the k-th, k + 1-st and k + 2-nd are close to one another, the whole row is decided again in float64
+// (choose64).  On random rows of 256 experts the former is one row in several hundred, the latter one in ten
+// thousand.  Where a group that is dropped may be above one that is kept (Ends), the groups' order is decided
+// in float64 (order64).  Without a bias the logits are compared, which is exact.
 template <int kN, bool kBiased>
 __global__ __launch_bounds__(256) void k_topk_wave(TopkArgs a, int log2_lanes, int vec) {
   const int lane = threadIdx.x & 63, cols = a.k + a.S;
@@ -505,18 +515,13 @@ __global__ __launch_bounds__(256) void k_topk_wave(TopkArgs a, int log2_lanes, i
         rank += u > v || (u == v && o < g);
       }
       if (by_score) {
-        // the last group kept and the first one dropped
-        const int last = __builtin_ctzll(__ballot(rank == a.KG - 1) | 1ull << 63);
-        const uint64_t out = __ballot(rank == a.KG && g < a.G);
-        if (out) {
-          const int first = __builtin_ctzll(out);
-          const auto at_lane = [](float f, int from) { return __uint_as_float(lane_value(__float_as_uint(f), from)); };
-          const float d = at_lane(v, first);
-          if (d > -kInf32 && close.groups(at_lane(v, last), d, at_lane(size, last), at_lane(size, first))) {
-            uint32_t hi[kN], lo[kN];
-            need_total();
-            rank = order64(a, at, l, b, score64, hi, lo);
-          }
+        // the least of the kept groups' lower ends, the largest of the dropped groups' upper ends
+        const Ends ends(v, size, close);
+        const uint32_t out = lane_value(wave_max63(rank >= a.KG && g < a.G ? ends.upper : 0u), 63);
+        if (out && ~lane_value(wave_max63(rank < a.KG && g < a.G ? ~ends.lower : 0u), 63) <= out) {
+          uint32_t hi[kN], lo[kN];
+          need_total();
+          rank = order64(a, at, l, b, score64, hi, lo);
         }
       }
       if (rank >= a.KG) {
@@ -754,13 +759,10 @@ __global__ __launch_bounds__(256) void k_topk_quarter(TopkArgs a, int log2_lanes
       });
       bool kept = before < a.KG << log2_lanes;
       if (by_score) {
-        // the last group kept and the first one dropped
-        const float last = value32(~row_max(kept ? ~key32(v) : 0u));
-        const uint32_t most = row_max(kept || v == -kInf32 ? 0u : key32(v));
-        const float first = value32(most);
-        // (sizes are not negative: their bits order as they do)
-        const float sizes = __uint_as_float(row_max(v == last || v == first ? __float_as_uint(size) : 0u));
-        const uint64_t which = __ballot(row < valid && most != 0 && close.groups(last, first, sizes, sizes));
+        // the least of the kept groups' lower ends, the largest of the dropped groups' upper ends
+        const Ends ends(v, size, close);
+        const uint32_t last = ~row_max(kept ? ~ends.lower : 0u), first = row_max(kept ? 0u : ends.upper);
+        const uint64_t which = __ballot(row < valid && first != 0 && last <= first);
         if (which) {
           for (int q = 0; q < 4; ++q) {
             if (!((which >> (16 * q)) & 0xFFFF)) continue;

@@ -513,6 +513,37 @@ def test_topk_group_sums_whose_terms_cancel(times, size, score):
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("size", [4096.0, 2.0 ** 20, 1.0e9, 2.0 ** 30])
+@pytest.mark.parametrize("E,G,KG,times", [(16, 4, 1, 1), (16, 4, 1, 41), (64, 8, 3, 1), (64, 8, 3, 41), (24, 3, 2, 1),
+                                          (24, 3, 2, 41), (256, 8, 4, 1), (256, 8, 4, 82), (1024, 8, 4, 1)])
+def test_topk_one_group_whose_terms_cancel_among_ordinary_ones(E, G, KG, times, size, score):
+    """One group has two experts with biases of opposite sign, so that its float32 sum is off by far more than
+    the sums of the other groups are apart, and may stand anywhere in their order."""
+    g = torch.Generator().manual_seed(E + G)
+    n = E // G
+    spread = min(1.5, size * 2.0 ** -23 * (E / 2 if score == "softmax" else 4))
+    logits = torch.randn(100, E, generator=g) * spread
+    for group in (0, G // 2, G - 1):
+        bias = torch.zeros(E)
+        bias[group * n:(group + 1) * n] = -float("inf")
+        bias[group * n], bias[group * n + 2] = size, -size
+        _check_topk(logits.cuda(), 3, bias.cuda(), times=times, score=score, num_groups=G, topk_groups=KG, group_top=2)
+
+
+@pytest.mark.parametrize("times", [1, 4096])
+def test_topk_cancelling_group_worked_by_hand(times):
+    """Two sigmoid scores of 0.952574 with biases of +-2^30: their sum is 1.905 and in float32 0, the best of the
+    other groups' is 1.32.  The other groups' experts are far apart, so that nothing else asks for 64 bits."""
+    logits = torch.tensor([0.0, 0.3, 0.2, 0.1] * 4)[None].clone()
+    logits[0, 0] = logits[0, 2] = 3.0
+    bias = torch.zeros(16)
+    bias[0], bias[2], bias[1], bias[3] = 2.0 ** 30, -2.0 ** 30, -float("inf"), -float("inf")
+    bias[4:8], bias[8:12] = 0.1, 0.05
+    idx, _ = _topk(logits.repeat(times, 1).cuda(), 2, bias.cuda(), score="sigmoid", num_groups=4, topk_groups=1, group_top=2)
+    assert torch.equal(idx.cpu(), torch.tensor([[0, 2]], dtype=torch.int32).expand(times, -1))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("G,KG,group_top", [(1, 1, 1), (4, 2, 1), (4, 2, 2)])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("E,times", [(32, 1), (32, 342), (256, 1), (256, 683), (1024, 1)])
