@@ -312,12 +312,15 @@ __device__ __forceinline__ void load_bias(const TopkArgs& a, int e0, int mine, b
 }
 
 // A chosen expert's weight before the renormalisation, 0 where there is none: in float32 (to 2^-18) unless one
-// of the row's is so small that float32's range or the renormalisation's 1e-20 would matter.
+// of the row's is so small that float32's range or the renormalisation's 1e-20 would matter.  row_lanes: the lanes
+// that hold this lane's row, whose neighbours' weights have no say in it.
 template <class Score32, class Score64>
-__device__ __forceinline__ double weight_of(bool has, float logit, const Score32& score32, const Score64& score64) {
+__device__ __forceinline__ double weight_of(bool has, float logit, uint64_t row_lanes, const Score32& score32, const Score64& score64) {
   const float s = has ? score32(logit) : 1.f;
-  if (__ballot(s < 1e-10f)) return has ? score64(logit) : 0.0;
-  return has ? (double)s : 0.0;
+  const uint64_t small = __ballot(s < 1e-10f);
+  double w = has ? (double)s : 0.0;
+  if (small) w = !(small & row_lanes) ? w : has ? score64(logit) : 0.0;
+  return w;
 }
 
 // Whether two float32 ordering values may be out of order (see k_topk_wave).
@@ -614,7 +617,7 @@ __global__ __launch_bounds__(256) void k_topk_wave(TopkArgs a, int log2_lanes, i
     }
     if (lane >= a.k) chosen = -1;
 
-    double s = weight_of(chosen >= 0, logit, score32, [&](float v) -> double {
+    double s = weight_of(chosen >= 0, logit, ~0ull, score32, [&](float v) -> double {
       if (a.sigmoid) return 1.0 / (1.0 + exp64(-(double)v));
       return (v == lmax ? 1.0 : exp64((double)v - (double)lmax)) * (double)unit;
     });
@@ -662,12 +665,13 @@ __global__ __launch_bounds__(256) void k_topk_quarter(TopkArgs a, int log2_lanes
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, quarter = lane >> 4, li = lane & 15, cols = a.k + a.S;
   const Spread at{log2_lanes, a.E / a.G};
   const int g = li >> log2_lanes, i0 = (li & ((1 << log2_lanes) - 1)) * kN, e0 = at.first(li, kN);
-  const int mine = g < a.G ? min(max(at.n - i0, 0), kN) : 0;
+  const int lane_experts = g < a.G ? min(max(at.n - i0, 0), kN) : 0;
   const bool by_score = kBiased || (a.G > 1 && a.group_top == 2);
   const int valid = a.num_valid ? min(a.T, *a.num_valid) : a.T;
   int* out = s_chosen[wave][quarter];
   for (int row0 = (blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(wave)) * 4; row0 < a.T; row0 += gridDim.x * 16) {
     const int row = row0 + quarter;
+    const int mine = row < valid ? lane_experts : 0;         // padding is not looked at
     const size_t base = (size_t)min(row, a.T - 1) * a.stride;
     float l[kN];
     load_lane(a, base + e0, mine, vec, l);
@@ -864,7 +868,7 @@ __global__ __launch_bounds__(256) void k_topk_quarter(TopkArgs a, int log2_lanes
     lds_done();                                  // read before the next rows' are written
     if (li >= a.k) chosen = -1;
 
-    double s = weight_of(chosen >= 0, logit, score32, [&](float v) -> double {
+    double s = weight_of(chosen >= 0, logit, 0xFFFFull << (16 * quarter), score32, [&](float v) -> double {
       if (a.sigmoid) return 1.0 / (1.0 + exp64(-(double)v));
       return (v == lmax ? 1.0 : exp64((double)v - (double)lmax)) * (double)unit;
     });

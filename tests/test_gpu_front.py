@@ -597,6 +597,32 @@ def test_topk_padded_rows(n):
     _check_topk(logits, 4, None, num_valid, num_shared=1, renorm=True)
 
 
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("score,biased", [("softmax", False), ("softmax", True), ("sigmoid", False), ("sigmoid", True)])
+@pytest.mark.parametrize("E,G,KG,group_top", [(64, 1, 1, 1), (96, 4, 2, 2), (256, 8, 4, 2)])
+def test_topk_rows_are_independent_of_their_neighbours_and_of_the_padding(E, G, KG, group_top, score, biased, renorm):
+    """A row's experts and weights, bit for bit, whatever lies in the other rows and behind the last valid one."""
+    g = torch.Generator().manual_seed(E + KG)
+    T, k, n = 8195, 6, 8190                                   # four rows a wave: 8188 and 8189 share theirs with padding
+    kw = dict(score=score, num_groups=G, topk_groups=KG, group_top=group_top, renorm=renorm)
+    logits = torch.randn(T, E, generator=g).cuda()
+    bias = (0.1 * torch.randn(E, generator=g)).cuda() if biased else None
+    num_valid = torch.tensor([n], dtype=torch.int32, device="cuda")
+    idx, w = _topk(logits, k, bias, num_valid, **dict(kw))
+    assert (idx[n:] == -1).all() and (w[n:] == 0).all()
+    for value in (-200.0, float("nan"), float("inf"), -float("inf"), torch.finfo(torch.float32).max):
+        other = logits.clone()
+        other[n:] = value
+        got_i, got_w = _topk(other, k, bias, num_valid, **dict(kw))
+        assert torch.equal(got_i, idx) and torch.equal(got_w.view(torch.int32), w.view(torch.int32)), f"padding of {value}"
+        other[1::4], other[2::4] = value, value               # every row's neighbours but these rows' own
+        keep = torch.arange(0, n, 4, device="cuda")
+        got_i, got_w = _topk(other, k, bias, num_valid, **dict(kw))
+        for r in (keep, keep[:-1] + 3):
+            assert torch.equal(got_i[r], idx[r]) and torch.equal(got_w[r].view(torch.int32), w[r].view(torch.int32)), \
+                f"neighbours of {value}"
+
+
 # ------------------------------------------------------------------------------------ together
 class Chain:
     """norm -> gate -> topk -> expert layer -> norm of the next layer, on buffers made once."""
