@@ -311,16 +311,38 @@ __device__ __forceinline__ void load_bias(const TopkArgs& a, int e0, int mine, b
   for (int j = 0; j < kN; ++j) b[j] = cleaned(b[j]);
 }
 
-// A chosen expert's weight before the renormalisation, 0 where there is none: in float32 (to 2^-18) unless one
-// of the row's is so small that float32's range or the renormalisation's 1e-20 would matter.  row_lanes: the lanes
-// that hold this lane's row, whose neighbours' weights have no say in it.
-template <class Score32, class Score64>
-__device__ __forceinline__ double weight_of(bool has, float logit, uint64_t row_lanes, const Score32& score32, const Score64& score64) {
-  const float s = has ? score32(logit) : 1.f;
-  const uint64_t small = __ballot(s < 1e-10f);
-  double w = has ? (double)s : 0.0;
-  if (small) w = !(small & row_lanes) ? w : has ? score64(logit) : 0.0;
-  return w;
+// exp(x) to 2^-33, for weights, which are rounded to 2^-24; |x| at most 1000.  As exp64 with a shorter series, of which
+// the terms from r^4 on, at most 2^-10 together, are float32, and as few steps after one another as it takes.
+__device__ __forceinline__ double exp_weight(double x) {
+  const double n = __builtin_rint(x * 1.4426950408889634), r = __builtin_fma(n, -0.6931471805599453, x), r2 = r * r;
+  const float f = (float)r, f2 = f * f;
+  const float a = __builtin_fmaf(f, 1.0f / 120.0f, 1.0f / 24.0f), b = __builtin_fmaf(f, 1.0f / 5040.0f, 1.0f / 720.0f),
+              c = __builtin_fmaf(f, 1.0f / 362880.0f, 1.0f / 40320.0f);
+  const float q = __builtin_fmaf(__builtin_fmaf(c, f2, b), f2, a);
+  const double p = __builtin_fma(__builtin_fma((double)q, r2, __builtin_fma(r, 1.0 / 6.0, 0.5)), r2, 1.0 + r);
+  return __builtin_ldexp(p, (int)n);
+}
+
+// 1 / y for a positive y whose reciprocal is a normal number: the hardware's estimate (2^-23) and a Newton step.
+__device__ __forceinline__ double reciprocal64(double y) {
+  const double e = __builtin_amdgcn_rcp(y);
+  return __builtin_fma(__builtin_fma(-y, e, 1.0), e, e);
+}
+
+// The weight of a lane's chosen expert, 0 where it has none, in float64 so that it is rounded once, to float32.  top,
+// total: the softmax's largest logit and its sum (0 where the scores decide nothing: it cancels under the renormalisation,
+// and the chosen hold so much of it that 1e-20 does not count); sum_of: the sum over the row's lanes.  Exponents stop at
+// +-700, beyond which a score is 0 or 1 all the same.
+template <class Sum>
+__device__ __forceinline__ double weight64(const TopkArgs& a, bool has, float logit, float top, double total, const Sum& sum_of) {
+  double s = 0.0;
+  if (has) {
+    if (a.sigmoid) s = reciprocal64(1.0 + exp_weight(-(double)__builtin_amdgcn_fmed3f(logit, -700.f, 700.f)));
+    else s = logit == top ? 1.0 : exp_weight(fmax((double)logit - (double)top, -700.0));     // infinities have no difference
+  }
+  if (a.renorm) total = sum_of(s) + (a.sigmoid ? 1e-20 : 1e-20 * total);
+  else if (a.sigmoid) return s;
+  return s > 0.0 ? s * reciprocal64(total) : 0.0;
 }
 
 // Whether two float32 ordering values may be out of order (see k_topk_wave).
@@ -416,6 +438,22 @@ __device__ __forceinline__ int choose64(const TopkArgs& a, const Spread& at, con
   return chosen;
 }
 
+// A lane's part of the softmax's sum, in float32: each term is off by up to (1 + |l - lmax|) 2^-23 of itself (the
+// difference and its product with log2 e are rounded, the exponential by a unit in the last place), their sum by
+// log2(kN) roundings.  The mean of |l - lmax| over the whole softmax is at most its entropy, so with lanes joined in
+// float64 the sum is off by less than (1 + ln 512 + 2) 2^-23 < 2^-19 of itself, and far less as errors vary.
+template <int kN>
+__device__ __forceinline__ float lane_sum(const float (&l)[kN], float lmax) {
+  float t[kN];
+#pragma unroll
+  for (int j = 0; j < kN; ++j) t[j] = l[j] == lmax ? 1.f : __expf(l[j] - lmax);
+#pragma unroll
+  for (int n = kN / 2; n > 0; n /= 2)
+#pragma unroll
+    for (int j = 0; j < n; ++j) t[j] += t[j + n];
+  return t[0];
+}
+
 // One wave per row, kN experts a lane.  Each round takes the largest key of the wave: a DPP maximum and a
 // ballot for the first lane that has it; lanes of up to four experts keep them sorted, and a round
 // moves the winner's up.
@@ -454,8 +492,9 @@ __global__ __launch_bounds__(256) void k_topk_wave(TopkArgs a, int log2_lanes, i
 #pragma unroll
       for (int j = 0; j < kN; ++j) b[j] = 0.f;
 
-    // the softmax's largest logit and, where the scores themselves are asked for, its sum
+    // the softmax's largest logit and, where scores are asked for, its sum
     float lmax = 0.f, unit = 1.f;                // unit: the largest score
+    double sum32 = 0.0;
     if (!a.sigmoid) {
       uint32_t top = 0;
 #pragma unroll
@@ -463,13 +502,9 @@ __global__ __launch_bounds__(256) void k_topk_wave(TopkArgs a, int log2_lanes, i
       const uint32_t k = lane_value(wave_max63(top), 63);
       lmax = k ? value32(k) : 0.f;
       if (by_score || !a.renorm) {
-        float t = 0.f;
-#pragma unroll
-        for (int j = 0; j < kN; ++j) t += l[j] == lmax ? 1.f : __expf(l[j] - lmax);
-        unit = __builtin_amdgcn_rcpf(__uint_as_float(lane_value(__float_as_uint(wave_sum63(t)), 63)));
+        sum32 = lane_value(wave_sum63((double)lane_sum(l, lmax)), 63);
+        unit = __builtin_amdgcn_rcpf((float)sum32);
       }
-      // renormalised and ordered by the logits: the sum cancels (the chosen ones hold at least 1/2048 of
-      // it, which 1e-20 does not change)
     }
     const auto score32 = [&](float v) -> float {
       if (a.sigmoid) return __builtin_amdgcn_rcpf(1.f + __expf(-v));
@@ -488,17 +523,18 @@ __global__ __launch_bounds__(256) void k_topk_wave(TopkArgs a, int log2_lanes, i
     }
 
     // the same in float64, for the rare rows that need it
+    const auto part64 = [&](float v) -> double { return v == lmax ? 1.0 : exp64((double)v - (double)lmax); };
     double total = 0.0;
     const auto need_total = [&] {
       if (a.sigmoid || total > 0.0) return;
       double t = 0.0;
 #pragma unroll
-      for (int j = 0; j < kN; ++j) t += l[j] == lmax ? 1.0 : exp64((double)l[j] - (double)lmax);
+      for (int j = 0; j < kN; ++j) t += part64(l[j]);
       total = lane_value(wave_sum63(t), 63);
     };
     const auto score64 = [&](float v) -> double {
       if (a.sigmoid) return 1.0 / (1.0 + exp64(-(double)v));
-      return (v == lmax ? 1.0 : exp64((double)v - (double)lmax)) / total;
+      return part64(v) / total;
     };
     const Close close = Close::of(a.sigmoid, unit);
     if (a.G > 1) {
@@ -617,11 +653,7 @@ __global__ __launch_bounds__(256) void k_topk_wave(TopkArgs a, int log2_lanes, i
     }
     if (lane >= a.k) chosen = -1;
 
-    double s = weight_of(chosen >= 0, logit, ~0ull, score32, [&](float v) -> double {
-      if (a.sigmoid) return 1.0 / (1.0 + exp64(-(double)v));
-      return (v == lmax ? 1.0 : exp64((double)v - (double)lmax)) * (double)unit;
-    });
-    if (a.renorm) s /= lane_value(wave_sum63(s), 63) + 1e-20;
+    const double s = weight64(a, chosen >= 0, logit, lmax, sum32, [](double v) { return lane_value(wave_sum63(v), 63); });
     if (lane < a.k) {
       idx[lane] = chosen;
       w[lane] = (float)(s * (double)a.scale);
@@ -679,6 +711,7 @@ __global__ __launch_bounds__(256) void k_topk_quarter(TopkArgs a, int log2_lanes
     if constexpr (kBiased) load_bias(a, e0, mine, vec, b);
 
     float lmax = 0.f, unit = 1.f;
+    double sum32 = 0.0;
     if (!a.sigmoid) {
       float top = l[0];
 #pragma unroll
@@ -686,12 +719,11 @@ __global__ __launch_bounds__(256) void k_topk_quarter(TopkArgs a, int log2_lanes
       const uint32_t k = row_max(top > -kInf32 ? key32(top) : 0u);
       lmax = k ? value32(k) : 0.f;
       if (by_score || !a.renorm) {
-        float t = 0.f;
-#pragma unroll
-        for (int j = 0; j < kN; ++j) t += l[j] == lmax ? 1.f : __expf(l[j] - lmax);
-        unit = __builtin_amdgcn_rcpf(row_sum(t));
+        sum32 = row_sum((double)lane_sum(l, lmax));
+        unit = __builtin_amdgcn_rcpf((float)sum32);
       }
     }
+    const auto part64 = [&](float v) -> double { return v == lmax ? 1.0 : exp64((double)v - (double)lmax); };
     const auto score32 = [&](float v) -> float {
       if (a.sigmoid) return __builtin_amdgcn_rcpf(1.f + __expf(-v));
       return (v == lmax ? 1.f : __expf(v - lmax)) * unit;
@@ -828,7 +860,7 @@ __global__ __launch_bounds__(256) void k_topk_quarter(TopkArgs a, int log2_lanes
         if (!a.sigmoid) {
           double t = 0.0;
 #pragma unroll
-          for (int j = 0; j < kN; ++j) t += l[j] == lmax ? 1.0 : exp64((double)l[j] - (double)lmax);
+          for (int j = 0; j < kN; ++j) t += part64(l[j]);
           total = row_sum(t);
         }
         const bool has = li <= a.k && chosen >= 0;
@@ -836,7 +868,7 @@ __global__ __launch_bounds__(256) void k_topk_quarter(TopkArgs a, int log2_lanes
         if (has) {
           const double b = a.bias[chosen];
           if (a.sigmoid) c = 1.0 / (1.0 + exp64(-(double)logit)) + b;
-          else c = (logit == lmax ? 1.0 : exp64((double)logit - (double)lmax)) / total + b;
+          else c = part64(logit) / total + b;
         }
         int rank = 0;
         Rotations<16>::each([&](auto n) {
@@ -868,11 +900,7 @@ __global__ __launch_bounds__(256) void k_topk_quarter(TopkArgs a, int log2_lanes
     lds_done();                                  // read before the next rows' are written
     if (li >= a.k) chosen = -1;
 
-    double s = weight_of(chosen >= 0, logit, 0xFFFFull << (16 * quarter), score32, [&](float v) -> double {
-      if (a.sigmoid) return 1.0 / (1.0 + exp64(-(double)v));
-      return (v == lmax ? 1.0 : exp64((double)v - (double)lmax)) * (double)unit;
-    });
-    if (a.renorm) s /= row_sum(s) + 1e-20;
+    const double s = weight64(a, chosen >= 0, logit, lmax, sum32, [](double v) { return row_sum(v); });
     if (row < a.T && li < cols) {
       int e = chosen;
       float w = (float)(s * (double)a.scale);

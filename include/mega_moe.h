@@ -395,6 +395,8 @@ typedef struct {
  *   the k experts with the largest c_e in these groups, in descending order, go to topk_idx[t, 0..k)
  *   w_e = s_e (without the bias), divided by the sum over the chosen + 1e-20 with
  *   MEGA_MOE_FLAG_TOPK_RENORM, times scale, go to topk_w
+ *   (in float64, rounded once to float32; up to 512 experts the softmax's sum is good to 2^-19 of itself, which
+ *   counts without the renormalisation, or where the chosen hold so little of it that 1e-20 does)
  * Order is decided as if c were computed in float64, without a bias in the order of l itself; of
  * equal ones the lowest id (group) comes first.  A logit that is NaN or -inf counts in no softmax and its
  * expert is never chosen; nor is one whose bias is NaN or -inf.  Experts with a logit of +inf share

@@ -623,6 +623,36 @@ def test_topk_rows_are_independent_of_their_neighbours_and_of_the_padding(E, G, 
                 f"neighbours of {value}"
 
 
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("score,biased", [("softmax", False), ("softmax", True), ("sigmoid", False), ("sigmoid", True)])
+@pytest.mark.parametrize("E,k,G,KG,group_top,times", [
+    (16, 2, 1, 1, 1, 1), (64, 6, 1, 1, 1, 1), (64, 6, 1, 1, 1, 21), (96, 8, 4, 2, 2, 1), (96, 8, 4, 2, 2, 21),
+    (256, 8, 8, 4, 2, 1), (256, 8, 8, 4, 2, 41), (384, 8, 1, 1, 1, 1), (600, 8, 1, 1, 1, 1)])
+def test_topk_weights_are_rounded_once(E, k, G, KG, group_top, times, score, biased, renorm):
+    """One rounding to float32, 2^-24 of the weight (half of 2^-149 below the normal numbers), of values in float64: a
+    series for the exponential to 2^-33, sums and reciprocals to 2^-46, so 2^-30 with room.  Without the
+    renormalisation the softmax's sum has float32 terms e^x: x is rounded as a difference and times log2 e, which is
+    2 |x| 2^-24 of the term, and the exponential by 2^-23; the terms' mean of |x| is at most the entropy, ln 600; up to
+    16 of them are added in float32, in four levels of 2^-24: at most (7.4 + 2) 2^-23 < 2^-19.  The same sum weighs the renormalisation's 1e-20, which counts where biases
+    push the chosen experts as low as in the last rows."""
+    g = torch.Generator().manual_seed(E + k)
+    logits = torch.randn(200, E, generator=g) * 3
+    logits[150:175] *= 12                                     # scores down to 1e-40
+    logits[175:, E // 2:] -= 40 + torch.arange(25)[:, None].float()
+    kw = dict(score=score, num_groups=G, topk_groups=KG, group_top=group_top, renorm=renorm, scale=2.5)
+    for low in (False, True) if biased else (False,):
+        bias = (torch.randn(E, generator=g) * 0.1) if biased else None
+        if low:
+            bias[E // 2:] += 2.0
+        idx, w = _topk((logits.repeat(times, 1)).cuda(), k, None if bias is None else bias.cuda(), **dict(kw))
+        ref_i, ref_w = front.gate_topk(_f64(logits), None if bias is None else _f64(bias), k, **kw)
+        assert np.array_equal(idx.cpu().numpy(), np.tile(ref_i, (times, 1)))
+        ref_w = np.tile(ref_w, (times, 1))
+        off = 2.0 ** -19 if score == "softmax" and (low or not renorm) else 2.0 ** -30
+        err = np.abs(_f64(w) - ref_w) - ((2.0 ** -24 + off) * np.abs(ref_w) + 2.0 ** -150)
+        assert (err <= 0).all(), f"{int((err > 0).sum())} of {err.size} weights"
+
+
 # ------------------------------------------------------------------------------------ together
 class Chain:
     """norm -> gate -> topk -> expert layer -> norm of the next layer, on buffers made once."""
