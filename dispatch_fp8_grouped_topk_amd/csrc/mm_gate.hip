@@ -5,6 +5,7 @@
 // 8 significant bits each (w = hi + mid + lo exactly, by truncation) and multiplied by three MFMAs
 // into the same sum.  A few logits are dot products of rows instead, with float32 multiply-adds (k_gate_rows).
 #include "mm_front.h"
+#include "mm_gate_policy.h"
 
 namespace mm {
 namespace {
@@ -363,50 +364,15 @@ hipError_t launch_rows(const GateArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Rows of a few tokens go to k_gate_rows as long as reading them again for each logit costs less than the
-// tiles' K loop of fixed length.  Measured (us, rows with one token a workgroup, with two, tiles; H 7168, E 256):
-// BF16 weights T 1 2.4, 2.7, 5.1; T 4 3.0, 3.0, 5.1; T 8 3.8, 3.7, 5.1; T 16 5.5, 4.9, 5.1; float32 T 1 2.5,
-// 2.7, 6.9; T 4 3.4, 3.3, 7.0; T 8 4.6, 4.2, 6.9; T 16 7.5, 6.1, 6.9.  T 32, E 64, H 4096 3.5, 3.4, 4.4; with few
-// experts the tiles win sooner: T 256, E 8, H 7168 6.3, 6.4, 5.0.
-constexpr int kRowsTokens = 64;
-constexpr long kRowsLogits = 2048;
-constexpr int kRowsSingle = 512;
-
-// The tile sizes built (experts, tokens).  A workgroup fetches its rows of both operands once, at 40 to
-// 50 bytes a clock and compute unit whatever the tile, so the time goes as the bytes of a tile's rows
-// times the rounds its workgroups need on 256 compute units; the smallest product wins, of equal
-// ones the smaller tile.  Measured (us, H 7168, E 256; the chosen tile, the next smaller, the next larger):
-// BF16 weights T 1 (without k_gate_rows) 5.1, -, 5.7; T 128 7.4, 10.9, 8.3 (8 x 16); T 1024 13.6, 20.5, 17.8 (32 x 32); T 2048 18.4,
-// 25.4, 23.2; T 4096 24.6, 34.9, 33.0; T 8192 49.6, 64.2, - (128 x 64); float32 weights T 1 6.7, -, 7.8;
-// T 128 // 9.9, 15.3, 10.7 (8 x 16); T 1024 20.7, 27.8, 25.3; T 8192 86.9, 120.3, - (64 x 128).
-struct Tile {
-  int e, t;
-};
-constexpr Tile kTilesBf16[] = {{8, 8}, {8, 16}, {16, 16}, {16, 32}, {32, 32}, {64, 32}, {64, 64}, {128, 64}};
-constexpr Tile kTilesF32[] = {{8, 8}, {8, 16}, {16, 16}, {16, 32}, {32, 32}, {32, 64}, {64, 128}};
-
-template <int kCount>
-int choose(const Tile (&tiles)[kCount], int weight_bytes, const GateArgs& a) {
-  int best = 0;
-  double least = 0;
-  for (int i = 0; i < kCount; ++i) {
-    const Tile t = tiles[i];
-    const long groups = (long)((a.E + t.e - 1) / t.e) * (((long)a.T + t.t - 1) / t.t);
-    const double cost = (double)((groups + 255) / 256) * (t.e * weight_bytes + t.t * 2);
-    if (i == 0 || cost < least) best = i, least = cost;
-  }
-  return best;
-}
-
 }  // namespace
 
+// The choice of kernel and tile is gate_variant's (mm_gate_policy.h).
 hipError_t launch_gate_logits(const GateArgs& a, hipStream_t s) {
-  if (a.T <= kRowsTokens && (long)a.T * a.E <= kRowsLogits) {
-    if (a.T == 1 || a.T * a.E <= kRowsSingle) return a.w_f32 ? launch_rows<true, 1>(a, s) : launch_rows<false, 1>(a, s);
-    return a.w_f32 ? launch_rows<true, 2>(a, s) : launch_rows<false, 2>(a, s);
-  }
+  const int v = gate_variant(a.T, a.E, a.w_f32 != 0);
+  if (v == kGateRowsSingle) return a.w_f32 ? launch_rows<true, 1>(a, s) : launch_rows<false, 1>(a, s);
+  if (v == kGateRowsPair) return a.w_f32 ? launch_rows<true, 2>(a, s) : launch_rows<false, 2>(a, s);
   if (a.w_f32) {
-    switch (choose(kTilesF32, 4, a)) {
+    switch (v) {
       case 0: return launch<true, 8, 8, 8, 6, 6, 1>(a, s);
       case 1: return launch<true, 8, 16, 16, 2, 2, 1>(a, s);
       case 2: return launch<true, 16, 16, 8, 2, 2, 1>(a, s);
@@ -416,7 +382,7 @@ hipError_t launch_gate_logits(const GateArgs& a, hipStream_t s) {
       default: return launch<true, 64, 128, 4, 1, 1, 4>(a, s);
     }
   }
-  switch (choose(kTilesBf16, 2, a)) {
+  switch (v) {
     case 0: return launch<false, 8, 8, 8, 9, 9, 1>(a, s);
     case 1: return launch<false, 8, 16, 8, 6, 6, 1>(a, s);
     case 2: return launch<false, 16, 16, 8, 4, 4, 1>(a, s);

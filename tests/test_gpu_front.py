@@ -307,6 +307,45 @@ def test_gate_logits_of_few_rows(T, H, E, w):
     assert torch.equal(_gate(xi, Wi).double(), (xi.cpu().double() @ Wi.cpu().double().t()).cuda())
 
 
+# every tile of both types of weights (test_gate_policy.py sees to that), ragged, with fewer steps of 64 columns than a
+# workgroup has waves and with steps that the waves do not share evenly
+GATE_TILES = [(31, 128, 130), (45, 1152, 130), (100, 1152, 200), (127, 128, 253), (65, 2176, 257), (140, 128, 255), (150, 1664, 250),
+              (300, 128, 250), (513, 1152, 161), (700, 128, 250), (1021, 7168, 255), (1000, 1664, 254), (1537, 128, 254),
+              (2047, 1152, 255), (1800, 7168, 256), (2050, 128, 253), (3001, 1152, 250), (4100, 128, 250),
+              (6001, 1152, 255), (8197, 128, 131), (9000, 1152, 130)]
+
+
+@pytest.mark.parametrize("w", ["bf16", "f32"])
+@pytest.mark.parametrize("T,H,E", GATE_TILES)
+def test_gate_logits_of_every_tile(T, H, E, w):
+    """Whole numbers exactly, random values within test_gate_logits_of_few_rows' bound."""
+    _say("gate tiles", T, H, E, w)
+    g = torch.Generator().manual_seed(T * 5 + E)
+    xi = _rows(torch.randint(-4, 5, (T, H), generator=g).to(torch.bfloat16).cuda(), 8 * (T % 3))
+    Wi = torch.randint(-8, 9, (E, H), generator=g).to(DT[w][1]).cuda()
+    assert torch.equal(_gate(xi, Wi).double(), (xi.cpu().double() @ Wi.cpu().double().t()).cuda())
+    x = _rows(torch.randn(T, H, generator=g).to(torch.bfloat16).cuda(), 8 * (E % 3))
+    W = (torch.randn(E, H, generator=g) * 0.02).to(DT[w][1]).cuda()
+    got = _f64(_gate(x, W))
+    ref, mag = front.gate_logits(_f64(x), _f64(W))
+    assert (np.abs(got - ref) <= (H * (3 if w == "f32" else 1) + 8) * 2.0 ** -23 * mag).all()
+
+
+GATE_BITS = [(31, 130), (127, 253), (140, 255), (300, 250), (700, 250), (1537, 254), (4100, 250)]
+
+
+@pytest.mark.parametrize("T,E", GATE_BITS)
+def test_gate_float32_weights_keep_all_their_bits_in_every_tile(T, E):
+    g = torch.Generator().manual_seed(T)
+    H = 384
+    W = (1 + torch.rand(E, H, generator=g)) * torch.exp2(torch.randint(-102, 100, (E, H), generator=g).float())
+    W = torch.where(torch.rand(E, H, generator=g) < 0.5, W, -W).cuda()
+    x = torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")
+    at = torch.arange(T, device="cuda") % H
+    x[torch.arange(T, device="cuda"), at] = 1.0
+    assert torch.equal(_gate(x, W), W.t()[at])
+
+
 @pytest.mark.parametrize("w", ["bf16", "f32"])
 @pytest.mark.parametrize("T", [1, 3, 6, 700])
 def test_gate_infinities_give_no_finite_logits(T, w):
