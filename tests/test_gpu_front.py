@@ -105,6 +105,15 @@ def test_norm_quant(T, H, x, w, residual, pad, recipe):
     _check_norm(got, X, R, W, recipe)
 
 
+@pytest.mark.parametrize("recipe", [0, 1, 2])
+@pytest.mark.parametrize("T,H,x,w,pad", [(3, 8320, "bf16", "f32", 8), (40, 16384, "bf16", "f32", 0),
+                                         (5, 9088, "f32", "bf16", 4), (3, 16384, "f32", "bf16", 0)])
+def test_norm_quant_of_long_rows_with_mixed_types(T, H, x, w, pad, recipe):
+    """More than 8192 columns: two chunks a thread."""
+    X, R, W = _norm_inputs(T, H, x, w, True, pad, seed=T + H)
+    _check_norm(_norm(X, R, W, recipe), X, R, W, recipe)
+
+
 @pytest.mark.parametrize("H", [128, 7168, 16384])
 @pytest.mark.parametrize("steps", [0, 1, 2, 5])
 def test_norm_power_of_two_scales_at_their_borders(H, steps):
