@@ -845,3 +845,43 @@ def test_binding_refusals_on_the_device():
     with pytest.raises(ValueError):
         mm.mega_moe_gate_topk(mm.TopkProblem.make(4, 256, 8), x, torch.zeros(4, 8, device="cuda"),
                               torch.zeros(4, 8, device="cuda"))
+
+
+def test_binding_refuses_other_strides_than_the_problems():
+    """Rows as far apart as the problem says, whatever the tensor's shape; a single row has no stride."""
+    T, H, E = 4, 256, 40
+    wide = torch.zeros(T, H + 16, dtype=torch.bfloat16, device="cuda")
+    x, tight = wide[:, :H], torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")
+    w, normed = torch.ones(H, dtype=torch.bfloat16, device="cuda"), torch.empty(T, H, dtype=torch.bfloat16, device="cuda")
+
+    def norm(x, residual=None, residual_out=None, **strides):
+        mm.mega_moe_norm_quant(mm.NormProblem.make(T, H, **strides), x, w, residual=residual, residual_out=residual_out,
+                               normed=normed)
+
+    norm(x, x_stride=H + 16)
+    norm(tight, x, x, residual_stride=H + 16)
+    for args, strides in (((x,), {}), ((tight,), dict(x_stride=H + 16)), ((x,), dict(x_stride=H + 8)),
+                          ((tight, x), {}), ((tight, tight, x), {}), ((tight, x, tight), dict(residual_stride=H + 16)),
+                          ((wide.t().contiguous().t()[:, :H],), dict(x_stride=H + 16))):
+        with pytest.raises(ValueError, match="expected"):
+            norm(*args, **strides)
+    mm.mega_moe_norm_quant(mm.NormProblem.make(1, H), x[:1], w, normed=normed[:1])
+
+    gate, logits = torch.zeros(E, H, dtype=torch.bfloat16, device="cuda"), torch.empty(T, E, device="cuda")
+    mm.mega_moe_gate_logits(mm.GateProblem.make(T, H, E, x_stride=H + 16), x, gate, logits)
+    for x_bad, weight, stride in ((x, gate, 0), (tight, gate, H + 16), (x, gate, H + 8),
+                                  (tight, torch.zeros(E, H + 8, dtype=torch.bfloat16, device="cuda")[:, :H], 0)):
+        with pytest.raises(ValueError, match="expected"):
+            mm.mega_moe_gate_logits(mm.GateProblem.make(T, H, E, x_stride=stride), x_bad, weight, logits)
+    with pytest.raises(ValueError, match="expected"):
+        mm.mega_moe_gate_logits(mm.GateProblem.make(T, H, E), tight, gate, torch.empty(T, E + 4, device="cuda")[:, :E])
+
+    far = torch.zeros(T, E + 3, device="cuda")[:, :E]
+    idx, tw = torch.empty(T, 2, dtype=torch.int32, device="cuda"), torch.empty(T, 2, device="cuda")
+    mm.mega_moe_gate_topk(mm.TopkProblem.make(T, E, 2, logits_stride=E + 3), far, idx, tw)
+    for l_bad, stride in ((far, 0), (logits, E + 3), (far, E + 4), (logits.t().contiguous().t(), 0)):
+        with pytest.raises(ValueError, match="expected"):
+            mm.mega_moe_gate_topk(mm.TopkProblem.make(T, E, 2, logits_stride=stride), l_bad, idx, tw)
+    with pytest.raises(ValueError, match="expected"):
+        mm.mega_moe_gate_topk(mm.TopkProblem.make(T, E, 2), logits, idx, torch.empty(2, T, device="cuda").t())
+    torch.cuda.synchronize()
