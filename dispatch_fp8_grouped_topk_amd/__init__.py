@@ -454,6 +454,8 @@ def _compiled():
     global _binding_module
     if _binding_module is None:
         _load()                              # torch and the library it links to
+        if not os.path.exists(os.path.join(HERE, "_binding.so")):
+            raise ImportError("_binding.so is missing; build it with `python -m dispatch_fp8_grouped_topk_amd.build`")
         from . import _binding as module
         _binding_module = module
     return _binding_module

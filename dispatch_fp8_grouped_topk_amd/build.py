@@ -1,7 +1,8 @@
 """Build libmegamoe.so (all HIP sources of csrc/) for gfx950 with hipcc, in place, and the compiled
 part of the Python binding, _binding.so (csrc/mm_binding.cpp, host code against torch's headers).
 
-    python -m dispatch_fp8_grouped_topk_amd.build
+    python -m dispatch_fp8_grouped_topk_amd.build                   # both
+    python -m dispatch_fp8_grouped_topk_amd.build --library-only    # the C library, which needs no torch
 
 Compiles every translation unit in parallel into _build/ and links the shared libraries
 next to this file.  Always recompiles (it is the package's "does it build" check).
@@ -72,11 +73,13 @@ def _link_binding(obj, torch_lib):
     os.replace(tmp, BINDING)
 
 
-def build(verbose: bool = True) -> str:
+def build(verbose: bool = True, binding: bool = True) -> str:
+    """The C library, with `binding` the compiled part of the Python binding too (torch's headers, a host C++ compiler).
+    The library is in place before a failure of the binding is raised."""
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
-        binding = ex.submit(_compile_binding)
+        bound = ex.submit(_compile_binding) if binding else None
         objs = list(ex.map(_compile, srcs))
     tmp = LIB + ".tmp"
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp]
@@ -84,11 +87,14 @@ def build(verbose: bool = True) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
-    _link_binding(*binding.result())
+    if bound is not None:
+        _link_binding(*bound.result())
     if verbose:
         print(f"built {LIB} from {len(srcs)} sources", file=sys.stderr)
     return LIB
 
 
 if __name__ == "__main__":
-    build()
+    if sys.argv[1:] not in ([], ["--library-only"]):
+        sys.exit("usage: build [--library-only]")
+    build(binding=not sys.argv[1:])
