@@ -885,3 +885,31 @@ def test_binding_refuses_other_strides_than_the_problems():
     with pytest.raises(ValueError, match="expected"):
         mm.mega_moe_gate_topk(mm.TopkProblem.make(T, E, 2), logits, idx, torch.empty(2, T, device="cuda").t())
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("T,E", [(37, 64), (8195, 64), (40, 600)])
+def test_topk_captured_batch_with_other_valid_rows_at_each_replay(T, E):
+    g = torch.Generator().manual_seed(T)
+    logits, bias = torch.randn(T, E, generator=g).cuda(), (0.1 * torch.randn(E, generator=g)).cuda()
+    n = torch.tensor([T], dtype=torch.int32, device="cuda")
+    p = mm.TopkProblem.make(T, E, 6, score=mm.SCORE_SIGMOID, num_groups=4, topk_groups=2, group_top=2, num_shared=1,
+                            flags=mm.FLAG_TOPK_RENORM)
+    idx, w = torch.empty(T, 7, dtype=torch.int32, device="cuda"), torch.empty(T, 7, device="cuda")
+    mm.mega_moe_gate_topk(p, logits, idx, w, bias=bias, num_valid=n)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mm.mega_moe_gate_topk(p, logits, idx, w, bias=bias, num_valid=n)
+    for valid in (T, T - 1, 0, T // 2, 1, T + 5):
+        logits.copy_(torch.randn(T, E, generator=g))
+        logits[max(valid, 0):] = float("nan")
+        n.fill_(valid)
+        eager_i, eager_w = _topk(logits, 6, bias, n, score="sigmoid", num_groups=4, topk_groups=2, group_top=2,
+                                 num_shared=1, renorm=True)
+        idx.fill_(-77)
+        w.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(idx, eager_i) and torch.equal(w, eager_w), valid
+        assert (idx[min(valid, T):] == -1).all() and (w[min(valid, T):] == 0).all()
+        assert (idx[:min(valid, T), 6] == E).all() and (idx[:min(valid, T)] >= 0).all()
