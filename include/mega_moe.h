@@ -303,11 +303,15 @@ int mega_moe_diag_mfma_block_sums(int fmt, const void* a, const void* b, const v
  * They need no workspace, allocate and synchronise nothing, keep nothing between calls and can be
  * captured into a HIP graph; each is one kernel launch on `stream` (a hipStream_t, NULL for the
  * default stream; the gate product: one for every 2^23 tokens), whose device has to be the current
- * one.  Pointers are device memory, 16-byte
- * aligned unless stated.  Arguments are validated synchronously, before the device is touched;
- * num_tokens == 0 is a valid no-op.  An output overlaps no input and no other output, from its
- * first element to its last, except where stated (INVALID_ARG).  Results are repeatable bit for bit.  Errors: INVALID_ARG, NULL_POINTER,
- * MISALIGNED, UNSUPPORTED_DEVICE, HIP. */
+ * one.  Pointers are device memory, 16-byte aligned unless stated.  Arguments are validated
+ * synchronously, before the device is touched; num_tokens == 0 is a valid no-op.  An output overlaps
+ * no input and no other output, from its first element to its last, except where stated
+ * (INVALID_ARG).
+ *
+ * The same call gives the same results bit for bit.  A row's outputs depend on its own inputs alone.
+ * Those of the norm and of the choice of experts do not depend on the row's place in the batch
+ * either (num_tokens may change the last bits of topk_w); those of the gate product as stated there.
+ * Errors: INVALID_ARG, NULL_POINTER, MISALIGNED, UNSUPPORTED_DEVICE, HIP. */
 typedef enum { MEGA_MOE_DTYPE_BF16 = 0, MEGA_MOE_DTYPE_F32 = 1 } mega_moe_dtype;
 typedef enum { MEGA_MOE_SCORE_SOFTMAX = 0, MEGA_MOE_SCORE_SIGMOID = 1 } mega_moe_score;
 
@@ -361,10 +365,12 @@ typedef struct {
 
 /* Gate product: logits[t, e] = sum_h x[t, h] * w[e, h], products exact, sums in float32.
  *   x bf16 [T, H], rows x_stride apart;  w [E, H] weight_dtype;  logits f32 [T, E]
- * Float32 weights are multiplied as they stand where there are few logits, otherwise as the sum of three
- * BF16 terms, which hold every float32 of magnitude 2^-102 or more exactly; with them an infinity in x or
- * w gives an infinity or NaN.  A value that is not finite affects only the logits of its row of x or of
- * its expert. */
+ * Float32 weights are multiplied as they stand where there are few logits (num_tokens at most 64 and num_tokens *
+ * num_experts at most 2048), otherwise as the sum of three BF16 terms, which hold every float32 of magnitude 2^-102
+ * or more exactly; with them an infinity in x or w gives an infinity or NaN, and smaller weights lose their last bits.
+ * The order of a logit's sum, and so its last bits, goes by num_tokens and by the row's place in the batch: a row among
+ * other rows need not give the bits that it gives alone.  A value that is not finite affects only the logits of its row
+ * of x or of its expert. */
 int mega_moe_gate_logits(const mega_moe_gate_problem* p, const void* x, const void* w, float* logits,
                          void* stream);
 
