@@ -694,8 +694,8 @@ struct Rotations {                               // f(n) for n = kN - 1 .. 1 as 
 // As k_topk_wave for many rows: four rows a wave, one on each 16 lanes, kN experts a lane, so that what
 // a row costs besides its experts is shared by four.  Each lane's keys are sorted once; a round takes the
 // row's largest head by a DPP maximum, and the lane that has it moves its keys up and leaves the expert
-// in LDS.  T 8192, E 256, k 8 of 4 of 8 groups, sigmoid and bias: 10.8 us, of which an empty launch is 2; bound
-// by the length of one wave's chain (about 2000 instructions for its four rows) at two waves a SIMD.
+// in LDS.  T 8192, E 256, k 8 of 4 of 8 groups, sigmoid and bias: 10.7 us, of which an empty launch is 2; bound
+// by the length of one wave's chain (1600 vector and 480 scalar instructions for its four rows) at two waves a SIMD.
 template <int kN, bool kBiased>
 __global__ __launch_bounds__(256) void k_topk_quarter(TopkArgs a, int log2_lanes, int vec) {
   __shared__ int s_chosen[4][4][16];             // by wave and row: the experts chosen; the groups kept
@@ -946,11 +946,16 @@ hipError_t launch_gate_topk(const TopkArgs& a, hipStream_t s) {
   int quarter_lanes = 4;
   while ((a.G << quarter_lanes) > 16 && quarter_lanes > 0) --quarter_lanes;
   const int quarter_need = (n + (1 << quarter_lanes) - 1) >> quarter_lanes;
-  // Four rows a wave take longer for one row and less for many.  Measured (us, k 8, quarter against wave;
-  // sigmoid and bias unless stated): E 64, T 2048 4.8 and 4.3, T 4096 4.9 and 5.4, T 8192 5.2 and 7.9; E 256,
-  // T 4096 8.0 and 6.8, T 8192 9.5 and 9.9, in 8 groups 10.8 and 11.5, softmax without a bias 7.1 and 7.5.
+  // Four rows a wave take longer for one row and less for many.  Measured (us, k 8, quarter against wave; sigmoid and
+  // bias unless stated) at T 2048, 3000, 4096, 5000, 6000, 7000, 8192:
+  //   E 64                      4.8 4.4, 4.9 4.8, 4.9 5.6, 5.2 6.0, 5.2 6.6, 5.2 7.4, 5.3 8.1
+  //   E 64, softmax, no bias    3.6 3.7, 3.6 4.0, 3.6 4.5, 4.0 5.0, 4.0 5.4, 4.0 6.0, 4.1 6.5
+  //   E 128                     5.5 4.8, 5.5 5.1, 5.5 6.1, 5.8 6.4, 6.3 7.2, 6.3 8.0, 6.3 8.8
+  //   E 256                     8.1 5.5, 8.2 6.1, 8.2 7.0, 8.8 7.5, 9.0 8.9, 9.1 9.6, 9.2 10.6
+  //   E 256, 4 of 8 groups      8.8 6.2, 8.9 6.8, 9.3 8.1, 10.0 8.8, 10.4 10.8, 10.4 11.4, 10.7 12.3
+  //   E 256, softmax, no bias   5.9 4.2, 6.0 4.6, 6.0 5.1, 6.3 5.6, 6.4 6.3, 6.5 7.0, 6.5 7.6
   // k + 2 experts have to fit 16 lanes.
-  if (a.T >= (quarter_need <= 8 ? 4096 : 8192) && a.G <= 16 && quarter_need <= 16 && a.k <= 14 && a.k + a.S <= 16) {
+  if (a.T >= (quarter_need <= 8 ? 4096 : 6144) && a.G <= 16 && quarter_need <= 16 && a.k <= 14 && a.k + a.S <= 16) {
     if (quarter_need <= 4) launch_quarter<4>(a, quarter_lanes, vec(4), s);
     else if (quarter_need <= 8) launch_quarter<8>(a, quarter_lanes, vec(8), s);
     else launch_quarter<16>(a, quarter_lanes, vec(16), s);
