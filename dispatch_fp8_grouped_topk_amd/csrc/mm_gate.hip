@@ -63,7 +63,7 @@ __device__ __forceinline__ void wait_vmcnt() {
 // part is multiplied the next one is read into registers, and its place in the ring is filled again
 // at once.
 //
-// T 8192, H 7168, E 256 (BF16 weights) takes 49 us: 614 TFLOP/s, of 21 us at the rate of a large matrix
+// T 8192, H 7168, E 256 (BF16 weights) takes 47.9 us: 628 TFLOP/s, of 21 us at the rate of a large matrix
 // product and 24 us for its bytes at that of a large copy.  Bound by fetching: 2.75 MB a compute unit,
 // at 36 bytes a clock with half the compute units busy (32 us) and 23 with all, where token rows come from HBM
 // through the same in-order queue (39 us when they lie in the last-level cache).  The matrix cores are
