@@ -2,7 +2,7 @@
 
 Argument marshalling only: torch tensors are passed to the C ABI (include/mega_moe.h) as raw
 device pointers together with the current HIP stream (through ctypes; for the operators in front
-of the layer through the compiled module _binding); every step of the layer runs in the
+of the layer and the layer in parts through the compiled module _binding); every step of the layer runs in the
 library's HIP kernels.  There is no fallback: if the shared library is missing or fails to
 load, importing the binding's functions raises.
 
@@ -21,6 +21,18 @@ and the operators in front of the layer, which make its inputs from a model's hi
                         q_sf=None, stream=None)
     mega_moe_gate_logits(problem, x, weight, logits, stream=None)
     mega_moe_gate_topk(problem, logits, topk_idx, topk_w, bias=None, num_valid=None, stream=None)
+
+and the layer in parts (tokens sorted by expert and back, the 8-bit product, the activation between two
+products), with the gradients of what stands between the router and the experts:
+
+    mega_moe_sort_workspace_size(problem) -> int
+    mega_moe_sort_tokens(problem, x, topk_idx, rows, pool_src, pair_pos, expert_offset, x_sf=None,
+                         rows_sf=None, workspace=None, stream=None)
+    mega_moe_unsort_tokens(problem, rows, pair_pos, y, topk_w=None, stream=None)
+    mega_moe_unsort_backward(problem, dy, pair_pos, rows=None, topk_w=None, d_rows=None, d_w=None, stream=None)
+    mega_moe_block_product(problem, x, x_sf, w, w_sf, y, group_offset=None, stream=None)
+    mega_moe_act_quant(problem, x, q=None, q_sf=None, out=None, num_valid=None, stream=None)
+    mega_moe_act_backward(problem, x, d_out, d_x, num_valid=None, stream=None)
 """
 from __future__ import annotations
 
@@ -46,8 +58,11 @@ FLAG_WEIGHT_E2M1_PAIRED = 128  # MXFP4: E2M1 weights in the row-pair layout of m
 
 DTYPE_BF16 = 0
 DTYPE_F32 = 1
+DTYPE_E4M3 = 2          # mega_moe_sort_tokens: 8-bit rows with their scales
 SCORE_SOFTMAX = 0
 SCORE_SIGMOID = 1
+ACT_NONE = 0
+ACT_SWIGLU = 1
 FLAG_TOPK_RENORM = 1    # TopkProblem: divide the chosen scores by their sum
 
 ABI_VERSION = 1
@@ -140,6 +155,77 @@ class TopkProblem(ctypes.Structure):
                    int(logits_stride))
 
 
+class SortProblem(ctypes.Structure):
+    """mega_moe_sort_problem."""
+    _fields_ = [
+        ("num_tokens", ctypes.c_int64),
+        ("hidden", ctypes.c_int32),
+        ("num_experts", ctypes.c_int32),
+        ("topk", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("recipe", ctypes.c_int32),
+        ("flags", ctypes.c_uint32),
+        ("x_stride", ctypes.c_int64),
+    ]
+
+    @classmethod
+    def make(cls, T, H, E, k, dtype=DTYPE_BF16, recipe=RECIPE_FP8_B128, flags=0, x_stride=0):
+        return cls(int(T), int(H), int(E), int(k), int(dtype), int(recipe), int(flags), int(x_stride))
+
+
+class UnsortProblem(ctypes.Structure):
+    """mega_moe_unsort_problem."""
+    _fields_ = [
+        ("num_tokens", ctypes.c_int64),
+        ("num_rows", ctypes.c_int64),
+        ("hidden", ctypes.c_int32),
+        ("topk", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("flags", ctypes.c_uint32),
+        ("stride", ctypes.c_int64),
+    ]
+
+    @classmethod
+    def make(cls, T, H, k, dtype=DTYPE_BF16, num_rows=0, flags=0, stride=0):
+        return cls(int(T), int(num_rows), int(H), int(k), int(dtype), int(flags), int(stride))
+
+
+class ProductProblem(ctypes.Structure):
+    """mega_moe_product_problem."""
+    _fields_ = [
+        ("num_rows", ctypes.c_int64),
+        ("n", ctypes.c_int32),
+        ("k", ctypes.c_int32),
+        ("num_groups", ctypes.c_int32),
+        ("flags", ctypes.c_uint32),
+        ("x_stride", ctypes.c_int64),
+        ("y_stride", ctypes.c_int64),
+    ]
+
+    @classmethod
+    def make(cls, M, N, K, G=1, flags=0, x_stride=0, y_stride=0):
+        return cls(int(M), int(N), int(K), int(G), int(flags), int(x_stride), int(y_stride))
+
+
+class ActProblem(ctypes.Structure):
+    """mega_moe_act_problem."""
+    _fields_ = [
+        ("num_rows", ctypes.c_int64),
+        ("width", ctypes.c_int32),
+        ("act", ctypes.c_int32),
+        ("recipe", ctypes.c_int32),
+        ("x_dtype", ctypes.c_int32),
+        ("swiglu_clamp", ctypes.c_float),
+        ("flags", ctypes.c_uint32),
+        ("x_stride", ctypes.c_int64),
+    ]
+
+    @classmethod
+    def make(cls, M, I, act=ACT_SWIGLU, recipe=RECIPE_FP8_B128, x_dtype=DTYPE_BF16, swiglu_clamp=0.0, flags=0,
+             x_stride=0):
+        return cls(int(M), int(I), int(act), int(recipe), int(x_dtype), float(swiglu_clamp), int(flags), int(x_stride))
+
+
 class _Views(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in
                 ("expert_count", "expert_offset", "pool_src", "pair_pos", "num_invalid",
@@ -191,6 +277,21 @@ def _load():
     lib.mega_moe_gate_logits.argtypes = [ctypes.POINTER(GateProblem), vp, vp, vp, vp]
     lib.mega_moe_gate_topk.restype = ctypes.c_int
     lib.mega_moe_gate_topk.argtypes = [ctypes.POINTER(TopkProblem), vp, vp, vp, vp, vp, vp]
+    lib.mega_moe_sort_workspace_size.restype = ctypes.c_int
+    lib.mega_moe_sort_workspace_size.argtypes = [ctypes.POINTER(SortProblem), ctypes.POINTER(ctypes.c_size_t)]
+    lib.mega_moe_sort_tokens.restype = ctypes.c_int
+    lib.mega_moe_sort_tokens.argtypes = [ctypes.POINTER(SortProblem), vp, vp, vp, vp, vp, vp, vp, vp, vp,
+                                         ctypes.c_size_t, vp]
+    lib.mega_moe_unsort_tokens.restype = ctypes.c_int
+    lib.mega_moe_unsort_tokens.argtypes = [ctypes.POINTER(UnsortProblem), vp, vp, vp, vp, vp]
+    lib.mega_moe_unsort_backward.restype = ctypes.c_int
+    lib.mega_moe_unsort_backward.argtypes = [ctypes.POINTER(UnsortProblem), vp, vp, vp, vp, vp, vp, vp]
+    lib.mega_moe_block_product.restype = ctypes.c_int
+    lib.mega_moe_block_product.argtypes = [ctypes.POINTER(ProductProblem), vp, vp, vp, vp, vp, vp, vp]
+    lib.mega_moe_act_quant.restype = ctypes.c_int
+    lib.mega_moe_act_quant.argtypes = [ctypes.POINTER(ActProblem), vp, vp, vp, vp, vp, vp]
+    lib.mega_moe_act_backward.restype = ctypes.c_int
+    lib.mega_moe_act_backward.argtypes = [ctypes.POINTER(ActProblem), vp, vp, vp, vp, vp]
     if lib.mega_moe_abi_version() != ABI_VERSION:
         raise ImportError(f"{LIB_PATH} has ABI {lib.mega_moe_abi_version()}, expected {ABI_VERSION}")
     _lib = lib
@@ -497,6 +598,66 @@ def mega_moe_gate_topk(problem: TopkProblem, logits, topk_idx, topk_w, bias=None
                                                    _handle(stream))
     if st:
         raise MegaMoEError(st, "mega_moe_gate_topk")
+
+
+def mega_moe_sort_workspace_size(problem: SortProblem) -> int:
+    out = ctypes.c_size_t(0)
+    st = _load().mega_moe_sort_workspace_size(ctypes.byref(problem), ctypes.byref(out))
+    if st:
+        raise MegaMoEError(st, "mega_moe_sort_workspace_size")
+    return out.value
+
+
+def mega_moe_sort_tokens(problem: SortProblem, x, topk_idx, rows, pool_src, pair_pos, expert_offset, x_sf=None,
+                         rows_sf=None, workspace=None, stream=None) -> None:
+    """Tokens sorted by expert (include/mega_moe.h): x [T, H] and rows [T*k, H] of the problem's dtype (uint8 with
+    x_sf and rows_sf for DTYPE_E4M3), or both None: the plan alone; topk_idx int32 [T, k]; pool_src int32 [T*k],
+    pair_pos int32 [T, k], expert_offset int32 [E + 1]; workspace of mega_moe_sort_workspace_size bytes."""
+    st = (_binding_module or _compiled()).sort_tokens(problem, x, x_sf, topk_idx, rows, rows_sf, pool_src, pair_pos,
+                                                     expert_offset, workspace, _handle(stream))
+    if st:
+        raise MegaMoEError(st, "mega_moe_sort_tokens")
+
+
+def mega_moe_unsort_tokens(problem: UnsortProblem, rows, pair_pos, y, topk_w=None, stream=None) -> None:
+    """y[t] = sum_j topk_w[t, j] rows[pair_pos[t, j]] (topk_w None: 1); without weights the gradient of the sort."""
+    st = (_binding_module or _compiled()).unsort_tokens(problem, rows, pair_pos, topk_w, y, _handle(stream))
+    if st:
+        raise MegaMoEError(st, "mega_moe_unsort_tokens")
+
+
+def mega_moe_unsort_backward(problem: UnsortProblem, dy, pair_pos, rows=None, topk_w=None, d_rows=None, d_w=None,
+                             stream=None) -> None:
+    """Gradients of mega_moe_unsort_tokens: d_rows [num_rows, H] and d_w float32 [T, k], each caller-allocated or None
+    (d_w needs rows)."""
+    st = (_binding_module or _compiled()).unsort_backward(problem, dy, rows, pair_pos, topk_w, d_rows, d_w,
+                                                         _handle(stream))
+    if st:
+        raise MegaMoEError(st, "mega_moe_unsort_backward")
+
+
+def mega_moe_block_product(problem: ProductProblem, x, x_sf, w, w_sf, y, group_offset=None, stream=None) -> None:
+    """y = x w^T in 8 bits with a scale for each block of 128, by group: x uint8 [M, K], x_sf float32 [M, K/128],
+    w uint8 [G, N, K], w_sf float32 [G, ceil(N/128), K/128], group_offset int32 [G + 1] on the device (None: one
+    group of every row), y bf16 [M, N] (caller-allocated; rows outside the groups are left as they were)."""
+    st = (_binding_module or _compiled()).block_product(problem, x, x_sf, w, w_sf, group_offset, y, _handle(stream))
+    if st:
+        raise MegaMoEError(st, "mega_moe_block_product")
+
+
+def mega_moe_act_quant(problem: ActProblem, x, q=None, q_sf=None, out=None, num_valid=None, stream=None) -> None:
+    """Activation (SwiGLU of x [M, 2I], or none of x [M, I]) to 8-bit rows q uint8 [M, I] with the recipe's scales
+    q_sf, and to out bf16 [M, I], each caller-allocated or None; num_valid int32 [1] on the device or None."""
+    st = (_binding_module or _compiled()).act_quant(problem, x, num_valid, q, q_sf, out, _handle(stream))
+    if st:
+        raise MegaMoEError(st, "mega_moe_act_quant")
+
+
+def mega_moe_act_backward(problem: ActProblem, x, d_out, d_x, num_valid=None, stream=None) -> None:
+    """Gradient of the SwiGLU: d_x [M, 2I] from x [M, 2I] and d_out [M, I], all of the problem's x_dtype."""
+    st = (_binding_module or _compiled()).act_backward(problem, x, d_out, num_valid, d_x, _handle(stream))
+    if st:
+        raise MegaMoEError(st, "mega_moe_act_backward")
 
 
 class MegaMoE:

@@ -12,6 +12,7 @@
 #include "mega_moe.h"
 #include "mm_common.h"
 #include "mm_front.h"
+#include "mm_parts.h"
 
 #define MM_EXPORT extern "C" __attribute__((visibility("default")))
 
@@ -592,4 +593,295 @@ MM_EXPORT int mega_moe_gate_topk(const mega_moe_topk_problem* p, const void* log
   a.scale = p->scale;
   a.shared_weight = p->shared_weight;
   return mm::launch_gate_topk(a, static_cast<hipStream_t>(stream)) == hipSuccess ? MEGA_MOE_OK : MEGA_MOE_ERR_HIP;
+}
+
+// ------------------------------------------------------------------------------- the layer in parts
+namespace {
+
+inline bool known_recipe(int r) {
+  return r == MEGA_MOE_RECIPE_FP8_B128 || r == MEGA_MOE_RECIPE_MXFP4W_B32 || r == MEGA_MOE_RECIPE_MXFP8_B32;
+}
+
+// Bytes of the scales of `rows` 8-bit rows.
+inline size_t scale_bytes(int recipe, int64_t rows, int64_t cols) {
+  return (size_t)rows * (recipe == MEGA_MOE_RECIPE_FP8_B128 ? cols / 128 * 4 : cols / 32);
+}
+
+// No output overlaps an input or another output.
+template <size_t I, size_t O>
+bool any_overlap(const Range (&in)[I], const Range (&out)[O]) {
+  for (size_t o = 0; o < O; ++o) {
+    for (const Range& r : in)
+      if (overlap(out[o], r)) return true;
+    for (size_t k = o + 1; k < O; ++k)
+      if (overlap(out[o], out[k])) return true;
+  }
+  return false;
+}
+
+int check_sort(const mega_moe_sort_problem* p) {
+  if (!p) return MEGA_MOE_ERR_NULL_POINTER;
+  if (p->num_tokens < 0 || p->num_tokens >= kMaxTokens || bad_hidden(p->hidden) || p->flags || p->num_experts < 1 ||
+      p->num_experts > mm::kMaxExperts || p->topk < 1 || p->topk > mm::kMaxTopk || !known_recipe(p->recipe))
+    return MEGA_MOE_ERR_INVALID_ARG;
+  if (p->num_tokens * p->topk >= kMaxTokens) return MEGA_MOE_ERR_INVALID_ARG;
+  if (!known_dtype(p->dtype) && p->dtype != MEGA_MOE_DTYPE_E4M3) return MEGA_MOE_ERR_INVALID_ARG;
+  const int64_t step = p->dtype == MEGA_MOE_DTYPE_E4M3 ? 16 : 16 / (int64_t)dtype_bytes(p->dtype);
+  return bad_stride(p->x_stride, p->hidden, step) ? MEGA_MOE_ERR_INVALID_ARG : MEGA_MOE_OK;
+}
+
+// The workspace: block counts, then the experts' totals.
+size_t sort_workspace(const mega_moe_sort_problem* p) {
+  const int64_t P = p->num_tokens * p->topk;
+  if (P <= mm::kSortSmallPairs) return 0;
+  return align256((size_t)mm::sort_blocks(P) * p->num_experts * 4) + align256((size_t)p->num_experts * 4);
+}
+
+int check_unsort(const mega_moe_unsort_problem* p) {
+  if (!p) return MEGA_MOE_ERR_NULL_POINTER;
+  if (p->num_tokens < 0 || p->num_tokens >= kMaxTokens || p->num_rows < 0 || p->num_rows > kMaxTokens ||
+      bad_hidden(p->hidden) || p->flags || p->topk < 1 || p->topk > mm::kMaxTopk || !known_dtype(p->dtype))
+    return MEGA_MOE_ERR_INVALID_ARG;
+  if (p->num_tokens * p->topk >= kMaxTokens) return MEGA_MOE_ERR_INVALID_ARG;
+  return bad_stride(p->stride, p->hidden, 16 / (int64_t)dtype_bytes(p->dtype)) ? MEGA_MOE_ERR_INVALID_ARG : MEGA_MOE_OK;
+}
+
+mm::UnsortArgs unsort_args(const mega_moe_unsort_problem* p) {
+  mm::UnsortArgs a{};
+  a.T = (int)p->num_tokens;
+  a.H = p->hidden;
+  a.k = p->topk;
+  a.R = (int)(p->num_rows ? p->num_rows : p->num_tokens * p->topk);
+  a.f32 = p->dtype == MEGA_MOE_DTYPE_F32;
+  a.stride = p->stride ? p->stride : p->hidden;
+  return a;
+}
+
+int check_act(const mega_moe_act_problem* p) {
+  if (!p) return MEGA_MOE_ERR_NULL_POINTER;
+  if (p->num_rows < 0 || p->num_rows >= kMaxTokens || bad_hidden(p->width) || !known_recipe(p->recipe) ||
+      !known_dtype(p->x_dtype) || (p->act != MEGA_MOE_ACT_NONE && p->act != MEGA_MOE_ACT_SWIGLU) ||
+      (p->flags & ~MEGA_MOE_FLAG_CLAMP_INPUTS) || std::isnan(p->swiglu_clamp) || p->swiglu_clamp < 0.f)
+    return MEGA_MOE_ERR_INVALID_ARG;
+  if (p->act == MEGA_MOE_ACT_NONE && (p->flags || p->swiglu_clamp != 0.f)) return MEGA_MOE_ERR_INVALID_ARG;
+  const int64_t cols = p->act == MEGA_MOE_ACT_SWIGLU ? 2 * (int64_t)p->width : p->width;
+  return bad_stride(p->x_stride, cols, 16 / (int64_t)dtype_bytes(p->x_dtype)) ? MEGA_MOE_ERR_INVALID_ARG : MEGA_MOE_OK;
+}
+
+mm::ActArgs act_args(const mega_moe_act_problem* p) {
+  mm::ActArgs a{};
+  a.M = (int)p->num_rows;
+  a.I = p->width;
+  a.swiglu = p->act == MEGA_MOE_ACT_SWIGLU;
+  a.x_stride = p->x_stride ? p->x_stride : (a.swiglu ? 2 * (int64_t)p->width : p->width);
+  a.clamp = std::isinf(p->swiglu_clamp) ? 0.f : p->swiglu_clamp;
+  a.clamp_inputs = (p->flags & MEGA_MOE_FLAG_CLAMP_INPUTS) != 0;
+  a.f32 = p->x_dtype == MEGA_MOE_DTYPE_F32;
+  a.per32 = p->recipe != MEGA_MOE_RECIPE_FP8_B128;
+  return a;
+}
+
+inline bool misaligned4(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 3u) != 0; }
+
+}  // namespace
+
+MM_EXPORT int mega_moe_sort_workspace_size(const mega_moe_sort_problem* p, size_t* bytes_out) {
+  const int st = check_sort(p);
+  if (st) return st;
+  if (!bytes_out) return MEGA_MOE_ERR_NULL_POINTER;
+  *bytes_out = sort_workspace(p);
+  return MEGA_MOE_OK;
+}
+
+MM_EXPORT int mega_moe_sort_tokens(const mega_moe_sort_problem* p, const void* x, const void* x_sf,
+                                   const int32_t* topk_idx, void* rows, void* rows_sf, int32_t* pool_src,
+                                   int32_t* pair_pos, int32_t* expert_offset, void* workspace, size_t workspace_bytes,
+                                   void* stream) {
+  const int bad = check_sort(p);
+  if (bad) return bad;
+  const int64_t T = p->num_tokens, H = p->hidden, E = p->num_experts, P = T * p->topk;
+  const bool bytes8 = p->dtype == MEGA_MOE_DTYPE_E4M3;
+  const size_t elem = bytes8 ? 1 : dtype_bytes(p->dtype);
+  if (!expert_offset) return MEGA_MOE_ERR_NULL_POINTER;
+  if (misaligned(expert_offset)) return MEGA_MOE_ERR_MISALIGNED;
+  mm::SortArgs a{};
+  a.offset = expert_offset;
+  a.E = (int)E;
+  if (T > 0) {
+    if (!topk_idx || !pool_src || !pair_pos || (!x) != (!rows)) return MEGA_MOE_ERR_NULL_POINTER;
+    if (x && bytes8 && (!x_sf || !rows_sf)) return MEGA_MOE_ERR_NULL_POINTER;
+    if ((!x || !bytes8) && (x_sf || rows_sf)) return MEGA_MOE_ERR_INVALID_ARG;
+    const void* ptrs[] = {x, x_sf, topk_idx, rows, rows_sf, pool_src, pair_pos, workspace};
+    for (const void* ptr : ptrs)
+      if (misaligned(ptr)) return MEGA_MOE_ERR_MISALIGNED;
+    const size_t need = sort_workspace(p);
+    if (need && (!workspace || workspace_bytes < need)) return MEGA_MOE_ERR_WORKSPACE_TOO_SMALL;
+    const int64_t xs = p->x_stride ? p->x_stride : H;
+    const Range in[] = {range_of(x, rows_bytes(T, xs, H, elem)), range_of(x_sf, scale_bytes(p->recipe, T, H)),
+                        range_of(topk_idx, (size_t)P * 4)};
+    const Range out[] = {range_of(rows, (size_t)P * H * elem), range_of(rows_sf, scale_bytes(p->recipe, P, H)),
+                         range_of(pool_src, (size_t)P * 4), range_of(pair_pos, (size_t)P * 4),
+                         range_of(expert_offset, (size_t)(E + 1) * 4), range_of(need ? workspace : nullptr, need)};
+    if (any_overlap(in, out)) return MEGA_MOE_ERR_INVALID_ARG;
+    a.x = x;
+    a.x_sf = static_cast<const uint32_t*>(x_sf);
+    a.idx = topk_idx;
+    a.rows = rows;
+    a.rows_sf = static_cast<uint32_t*>(rows_sf);
+    a.src = pool_src;
+    a.pos = pair_pos;
+    a.x_stride = (size_t)xs * elem;
+    a.T = (int)T;
+    a.k = p->topk;
+    a.P = (int)P;
+    a.row_bytes = (int)(H * elem);
+    a.sf_words = (int)(H / 128);               // a float, or four codes, for each 128 columns
+    if (need) {
+      a.NB = mm::sort_blocks(P);
+      a.block_pairs = mm::sort_block_pairs(P);
+      a.blk = static_cast<int32_t*>(workspace);
+      a.total = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + align256((size_t)a.NB * E * 4));
+    }
+  }
+  const int st = check_device();
+  if (st) return st;
+  return mm::launch_sort(a, static_cast<hipStream_t>(stream)) == hipSuccess ? MEGA_MOE_OK : MEGA_MOE_ERR_HIP;
+}
+
+MM_EXPORT int mega_moe_unsort_tokens(const mega_moe_unsort_problem* p, const void* rows, const int32_t* pair_pos,
+                                     const float* topk_w, void* y, void* stream) {
+  const int bad = check_unsort(p);
+  if (bad) return bad;
+  if (p->num_tokens == 0) return MEGA_MOE_OK;
+  if (!rows || !pair_pos || !y) return MEGA_MOE_ERR_NULL_POINTER;
+  if (misaligned(rows) || misaligned(pair_pos) || misaligned(topk_w) || misaligned(y)) return MEGA_MOE_ERR_MISALIGNED;
+  mm::UnsortArgs a = unsort_args(p);
+  const size_t elem = dtype_bytes(p->dtype), pairs = (size_t)a.T * a.k * 4;
+  const Range in[] = {range_of(rows, (size_t)a.R * a.H * elem), range_of(pair_pos, pairs), range_of(topk_w, pairs)};
+  const Range out[] = {range_of(y, rows_bytes(a.T, a.stride, a.H, elem))};
+  if (any_overlap(in, out)) return MEGA_MOE_ERR_INVALID_ARG;
+  const int st = check_device();
+  if (st) return st;
+  a.rows = rows;
+  a.pos = pair_pos;
+  a.w = topk_w;
+  a.y = y;
+  return mm::launch_unsort(a, static_cast<hipStream_t>(stream)) == hipSuccess ? MEGA_MOE_OK : MEGA_MOE_ERR_HIP;
+}
+
+MM_EXPORT int mega_moe_unsort_backward(const mega_moe_unsort_problem* p, const void* dy, const void* rows,
+                                       const int32_t* pair_pos, const float* topk_w, void* d_rows, float* d_w,
+                                       void* stream) {
+  const int bad = check_unsort(p);
+  if (bad) return bad;
+  if (p->num_tokens == 0) return MEGA_MOE_OK;
+  if (!dy || !pair_pos || (d_w && !rows)) return MEGA_MOE_ERR_NULL_POINTER;
+  if (!d_rows && !d_w) return MEGA_MOE_ERR_INVALID_ARG;
+  const void* ptrs[] = {dy, rows, pair_pos, topk_w, d_rows, d_w};
+  for (const void* ptr : ptrs)
+    if (misaligned(ptr)) return MEGA_MOE_ERR_MISALIGNED;
+  mm::UnsortArgs a = unsort_args(p);
+  const size_t elem = dtype_bytes(p->dtype), pairs = (size_t)a.T * a.k * 4, all = (size_t)a.R * a.H * elem;
+  // in place: each thread has read its own columns of a pair's row before it writes them
+  const Range in[] = {range_of(dy, rows_bytes(a.T, a.stride, a.H, elem)), range_of(d_rows == rows ? nullptr : rows, all),
+                      range_of(pair_pos, pairs), range_of(topk_w, pairs)};
+  const Range out[] = {range_of(d_rows, all), range_of(d_w, pairs)};
+  if (any_overlap(in, out)) return MEGA_MOE_ERR_INVALID_ARG;
+  const int st = check_device();
+  if (st) return st;
+  a.dy = dy;
+  a.rows = rows;
+  a.pos = pair_pos;
+  a.w = topk_w;
+  a.d_rows = d_rows;
+  a.d_w = d_w;
+  return mm::launch_unsort_backward(a, static_cast<hipStream_t>(stream)) == hipSuccess ? MEGA_MOE_OK : MEGA_MOE_ERR_HIP;
+}
+
+MM_EXPORT int mega_moe_block_product(const mega_moe_product_problem* p, const void* x, const float* x_sf, const void* w,
+                                     const float* w_sf, const int32_t* group_offset, void* y, void* stream) {
+  if (!p) return MEGA_MOE_ERR_NULL_POINTER;
+  if (p->num_rows < 0 || p->num_rows >= kMaxTokens || p->n <= 0 || p->n % 8 || p->n > mm::kMaxProductN || bad_hidden(p->k) ||
+      p->num_groups < 1 || p->num_groups > mm::kMaxExperts || p->flags || bad_stride(p->x_stride, p->k, 16) ||
+      p->x_stride > mm::kMaxProductStride || bad_stride(p->y_stride, p->n, 8))
+    return MEGA_MOE_ERR_INVALID_ARG;
+  const int64_t M = p->num_rows, N = p->n, K = p->k, G = p->num_groups;
+  if (M == 0) return MEGA_MOE_OK;
+  if (!x || !x_sf || !w || !w_sf || !y || (G > 1 && !group_offset)) return MEGA_MOE_ERR_NULL_POINTER;
+  if (misaligned(x) || misaligned(x_sf) || misaligned(w) || misaligned(w_sf) || misaligned(y) || misaligned4(group_offset))
+    return MEGA_MOE_ERR_MISALIGNED;
+  const int64_t xs = p->x_stride ? p->x_stride : K, ys = p->y_stride ? p->y_stride : N;
+  const Range in[] = {range_of(x, rows_bytes(M, xs, K, 1)), range_of(x_sf, (size_t)M * (K / 128) * 4),
+                      range_of(w, (size_t)G * N * K), range_of(w_sf, (size_t)G * ((N + 127) / 128) * (K / 128) * 4),
+                      range_of(group_offset, (size_t)(G + 1) * 4)};
+  const Range out[] = {range_of(y, rows_bytes(M, ys, N, 2))};
+  if (any_overlap(in, out)) return MEGA_MOE_ERR_INVALID_ARG;
+  const int st = check_device();
+  if (st) return st;
+  mm::ProductArgs a{};
+  a.x = static_cast<const uint8_t*>(x);
+  a.x_sf = x_sf;
+  a.w = static_cast<const uint8_t*>(w);
+  a.w_sf = w_sf;
+  a.offset = group_offset;
+  a.y = static_cast<uint16_t*>(y);
+  a.x_stride = xs;
+  a.y_stride = ys;
+  a.M = (int)M;
+  a.N = (int)N;
+  a.K = (int)K;
+  a.G = (int)G;
+  a.cus = device_cus();
+  if (!a.cus) return MEGA_MOE_ERR_HIP;
+  return mm::launch_product(a, static_cast<hipStream_t>(stream)) == hipSuccess ? MEGA_MOE_OK : MEGA_MOE_ERR_HIP;
+}
+
+MM_EXPORT int mega_moe_act_quant(const mega_moe_act_problem* p, const void* x, const int32_t* num_valid, void* q,
+                                 void* q_sf, void* out, void* stream) {
+  const int bad = check_act(p);
+  if (bad) return bad;
+  if (p->num_rows == 0) return MEGA_MOE_OK;
+  if (!x || (!q) != (!q_sf)) return MEGA_MOE_ERR_NULL_POINTER;
+  if (!q && !out) return MEGA_MOE_ERR_INVALID_ARG;
+  if (misaligned(x) || misaligned(q) || misaligned(q_sf) || misaligned(out) || misaligned4(num_valid))
+    return MEGA_MOE_ERR_MISALIGNED;
+  mm::ActArgs a = act_args(p);
+  const int64_t M = a.M, I = a.I;
+  const Range in[] = {range_of(x, rows_bytes(M, a.x_stride, a.swiglu ? 2 * I : I, dtype_bytes(p->x_dtype))),
+                      range_of(num_valid, 4)};
+  const Range outs[] = {range_of(q, (size_t)M * I), range_of(q_sf, scale_bytes(p->recipe, M, I)),
+                        range_of(out, (size_t)M * I * 2)};
+  if (any_overlap(in, outs)) return MEGA_MOE_ERR_INVALID_ARG;
+  const int st = check_device();
+  if (st) return st;
+  a.x = x;
+  a.num_valid = num_valid;
+  a.q = static_cast<uint8_t*>(q);
+  a.q_sf = q_sf;
+  a.out = static_cast<uint16_t*>(out);
+  return mm::launch_act_quant(a, static_cast<hipStream_t>(stream)) == hipSuccess ? MEGA_MOE_OK : MEGA_MOE_ERR_HIP;
+}
+
+MM_EXPORT int mega_moe_act_backward(const mega_moe_act_problem* p, const void* x, const void* d_out,
+                                    const int32_t* num_valid, void* d_x, void* stream) {
+  const int bad = check_act(p);
+  if (bad) return bad;
+  if (p->act != MEGA_MOE_ACT_SWIGLU) return MEGA_MOE_ERR_INVALID_ARG;
+  if (p->num_rows == 0) return MEGA_MOE_OK;
+  if (!x || !d_out || !d_x) return MEGA_MOE_ERR_NULL_POINTER;
+  if (misaligned(x) || misaligned(d_out) || misaligned(d_x) || misaligned4(num_valid)) return MEGA_MOE_ERR_MISALIGNED;
+  mm::ActArgs a = act_args(p);
+  const size_t elem = dtype_bytes(p->x_dtype), wide = rows_bytes(a.M, a.x_stride, 2 * (int64_t)a.I, elem);
+  // in place: each thread has read its own columns before it writes them
+  const Range in[] = {range_of(d_x == x ? nullptr : x, wide), range_of(d_out, (size_t)a.M * a.I * elem),
+                      range_of(num_valid, 4)};
+  const Range out[] = {range_of(d_x, wide)};
+  if (any_overlap(in, out)) return MEGA_MOE_ERR_INVALID_ARG;
+  const int st = check_device();
+  if (st) return st;
+  a.x = x;
+  a.num_valid = num_valid;
+  a.d_out = d_out;
+  a.d_x = d_x;
+  return mm::launch_act_backward(a, static_cast<hipStream_t>(stream)) == hipSuccess ? MEGA_MOE_OK : MEGA_MOE_ERR_HIP;
 }

@@ -1,11 +1,17 @@
-// Compiled part of the Python binding: the operators in front of the expert layer, which cost a few
-// microseconds each, so that their arguments are checked and marshalled in well under one.  It
+// Compiled part of the Python binding: the operators in front of the expert layer and the layer in parts, which cost
+// a few microseconds each, so that their arguments are checked and marshalled in well under one.  It
 // checks torch tensors against the problem, takes the stream and calls the C ABI (mega_moe.h); the
 // status goes back to Python.  No arithmetic happens here.
 //
 // norm_quant(problem, x, weight, residual, residual_out, normed, q, q_sf, stream) -> status
 // gate_logits(problem, x, weight, logits, stream) -> status
 // gate_topk(problem, logits, topk_idx, topk_w, bias, num_valid, stream) -> status
+// sort_tokens(problem, x, x_sf, topk_idx, rows, rows_sf, pool_src, pair_pos, expert_offset, workspace, stream) -> status
+// unsort_tokens(problem, rows, pair_pos, topk_w, y, stream) -> status
+// unsort_backward(problem, dy, rows, pair_pos, topk_w, d_rows, d_w, stream) -> status
+// block_product(problem, x, x_sf, w, w_sf, group_offset, y, stream) -> status
+// act_quant(problem, x, num_valid, q, q_sf, out, stream) -> status
+// act_backward(problem, x, d_out, num_valid, d_x, stream) -> status
 //
 // problem: a ctypes structure; stream: an int handle, or None for the current stream of the
 // tensors' device, which is made the current device for the call.
@@ -176,10 +182,144 @@ PyObject* gate_topk(PyObject*, PyObject* const* v, Py_ssize_t n) {
   });
 }
 
+// Scales that go with `rows` 8-bit rows of `cols` columns.
+void check_scales(const char* name, const at::Tensor* t, at::Device dev, int recipe, int64_t rows, int64_t cols) {
+  if (recipe == MEGA_MOE_RECIPE_FP8_B128) check_buffer(name, t, dev, at::kFloat, {rows, cols / 128});
+  else check_buffer(name, t, dev, at::kByte, {rows, cols / 32});
+}
+
+PyObject* sort_tokens(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  return guarded("sort_tokens", n, 11, [&] {
+    const auto p = problem_of<mega_moe_sort_problem>(v[0]);
+    const at::Tensor *x = tensor(v[1], "x", true), *x_sf = tensor(v[2], "x_sf", true), *idx = tensor(v[3], "topk_idx"),
+                     *rows = tensor(v[4], "rows", true), *rows_sf = tensor(v[5], "rows_sf", true),
+                     *src = tensor(v[6], "pool_src"), *pos = tensor(v[7], "pair_pos"),
+                     *offset = tensor(v[8], "expert_offset"), *ws = tensor(v[9], "workspace", true);
+    const at::Device dev = device_of(*idx, "mega_moe_sort_tokens");
+    const int64_t T = p.num_tokens, H = p.hidden, k = p.topk, pairs[] = {T, k};
+    const at::ScalarType type = p.dtype == MEGA_MOE_DTYPE_E4M3 ? at::kByte : type_of(p.dtype);
+    check_rows("x", x, dev, type, T, H, p.x_stride);
+    check_buffer("topk_idx", idx, dev, at::kInt, pairs);
+    check_buffer("rows", rows, dev, type, {T * k, H});
+    check_scales("x_sf", x_sf, dev, p.recipe, T, H);
+    check_scales("rows_sf", rows_sf, dev, p.recipe, T * k, H);
+    check_buffer("pool_src", src, dev, at::kInt, {T * k});
+    check_buffer("pair_pos", pos, dev, at::kInt, pairs);
+    check_buffer("expert_offset", offset, dev, at::kInt, {(int64_t)p.num_experts + 1});
+    if (ws && (ws->device() != dev || !ws->is_contiguous())) throw Refused("workspace must be a contiguous tensor on the same device");
+    void* s = stream_of(v[10], dev);
+    c10::DeviceGuard guard(dev);
+    return mega_moe_sort_tokens(&p, ptr(x), ptr(x_sf), static_cast<const int32_t*>(ptr(idx)), ptr(rows), ptr(rows_sf),
+                                static_cast<int32_t*>(ptr(src)), static_cast<int32_t*>(ptr(pos)),
+                                static_cast<int32_t*>(ptr(offset)), ptr(ws), ws ? ws->nbytes() : 0, s);
+  });
+}
+
+PyObject* unsort_tokens(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  return guarded("unsort_tokens", n, 6, [&] {
+    const auto p = problem_of<mega_moe_unsort_problem>(v[0]);
+    const at::Tensor *rows = tensor(v[1], "rows"), *pos = tensor(v[2], "pair_pos"), *w = tensor(v[3], "topk_w", true),
+                     *y = tensor(v[4], "y");
+    const at::Device dev = device_of(*pos, "mega_moe_unsort_tokens");
+    const int64_t T = p.num_tokens, H = p.hidden, k = p.topk, pairs[] = {T, k};
+    check_buffer("rows", rows, dev, type_of(p.dtype), {p.num_rows ? p.num_rows : T * k, H});
+    check_buffer("pair_pos", pos, dev, at::kInt, pairs);
+    check_buffer("topk_w", w, dev, at::kFloat, pairs);
+    check_rows("y", y, dev, type_of(p.dtype), T, H, p.stride);
+    void* s = stream_of(v[5], dev);
+    c10::DeviceGuard guard(dev);
+    return mega_moe_unsort_tokens(&p, ptr(rows), static_cast<const int32_t*>(ptr(pos)),
+                                  static_cast<const float*>(ptr(w)), ptr(y), s);
+  });
+}
+
+PyObject* unsort_backward(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  return guarded("unsort_backward", n, 8, [&] {
+    const auto p = problem_of<mega_moe_unsort_problem>(v[0]);
+    const at::Tensor *dy = tensor(v[1], "dy"), *rows = tensor(v[2], "rows", true), *pos = tensor(v[3], "pair_pos"),
+                     *w = tensor(v[4], "topk_w", true), *d_rows = tensor(v[5], "d_rows", true),
+                     *d_w = tensor(v[6], "d_w", true);
+    const at::Device dev = device_of(*pos, "mega_moe_unsort_backward");
+    const int64_t T = p.num_tokens, H = p.hidden, k = p.topk, pairs[] = {T, k};
+    const int64_t R = p.num_rows ? p.num_rows : T * k, all[] = {R, H};
+    check_rows("dy", dy, dev, type_of(p.dtype), T, H, p.stride);
+    check_buffer("rows", rows, dev, type_of(p.dtype), all);
+    check_buffer("pair_pos", pos, dev, at::kInt, pairs);
+    check_buffer("topk_w", w, dev, at::kFloat, pairs);
+    check_buffer("d_rows", d_rows, dev, type_of(p.dtype), all);
+    check_buffer("d_w", d_w, dev, at::kFloat, pairs);
+    void* s = stream_of(v[7], dev);
+    c10::DeviceGuard guard(dev);
+    return mega_moe_unsort_backward(&p, ptr(dy), ptr(rows), static_cast<const int32_t*>(ptr(pos)),
+                                    static_cast<const float*>(ptr(w)), ptr(d_rows), static_cast<float*>(ptr(d_w)), s);
+  });
+}
+
+PyObject* block_product(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  return guarded("block_product", n, 8, [&] {
+    const auto p = problem_of<mega_moe_product_problem>(v[0]);
+    const at::Tensor *x = tensor(v[1], "x"), *x_sf = tensor(v[2], "x_sf"), *w = tensor(v[3], "w"),
+                     *w_sf = tensor(v[4], "w_sf"), *offset = tensor(v[5], "group_offset", true), *y = tensor(v[6], "y");
+    const at::Device dev = device_of(*x, "mega_moe_block_product");
+    const int64_t M = p.num_rows, N = p.n, K = p.k, G = p.num_groups;
+    check_rows("x", x, dev, at::kByte, M, K, p.x_stride);
+    check_buffer("x_sf", x_sf, dev, at::kFloat, {M, K / 128});
+    check_buffer("w", w, dev, at::kByte, {G, N, K});
+    check_buffer("w_sf", w_sf, dev, at::kFloat, {G, (N + 127) / 128, K / 128});
+    check_buffer("group_offset", offset, dev, at::kInt, {G + 1});
+    check_rows("y", y, dev, at::kBFloat16, M, N, p.y_stride);
+    void* s = stream_of(v[7], dev);
+    c10::DeviceGuard guard(dev);
+    return mega_moe_block_product(&p, ptr(x), static_cast<const float*>(ptr(x_sf)), ptr(w),
+                                  static_cast<const float*>(ptr(w_sf)), static_cast<const int32_t*>(ptr(offset)), ptr(y), s);
+  });
+}
+
+PyObject* act_quant(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  return guarded("act_quant", n, 7, [&] {
+    const auto p = problem_of<mega_moe_act_problem>(v[0]);
+    const at::Tensor *x = tensor(v[1], "x"), *num_valid = tensor(v[2], "num_valid", true), *q = tensor(v[3], "q", true),
+                     *q_sf = tensor(v[4], "q_sf", true), *out = tensor(v[5], "out", true);
+    const at::Device dev = device_of(*x, "mega_moe_act_quant");
+    const int64_t M = p.num_rows, I = p.width, shape[] = {M, I};
+    check_rows("x", x, dev, type_of(p.x_dtype), M, p.act == MEGA_MOE_ACT_SWIGLU ? 2 * I : I, p.x_stride);
+    check_buffer("num_valid", num_valid, dev, at::kInt, {1});
+    check_buffer("q", q, dev, at::kByte, shape);
+    check_scales("q_sf", q_sf, dev, p.recipe, M, I);
+    check_buffer("out", out, dev, at::kBFloat16, shape);
+    void* s = stream_of(v[6], dev);
+    c10::DeviceGuard guard(dev);
+    return mega_moe_act_quant(&p, ptr(x), static_cast<const int32_t*>(ptr(num_valid)), ptr(q), ptr(q_sf), ptr(out), s);
+  });
+}
+
+PyObject* act_backward(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  return guarded("act_backward", n, 6, [&] {
+    const auto p = problem_of<mega_moe_act_problem>(v[0]);
+    const at::Tensor *x = tensor(v[1], "x"), *d_out = tensor(v[2], "d_out"), *num_valid = tensor(v[3], "num_valid", true),
+                     *d_x = tensor(v[4], "d_x");
+    const at::Device dev = device_of(*x, "mega_moe_act_backward");
+    const int64_t M = p.num_rows, I = p.width;
+    check_rows("x", x, dev, type_of(p.x_dtype), M, 2 * I, p.x_stride);
+    check_buffer("d_out", d_out, dev, type_of(p.x_dtype), {M, I});
+    check_buffer("num_valid", num_valid, dev, at::kInt, {1});
+    check_rows("d_x", d_x, dev, type_of(p.x_dtype), M, 2 * I, p.x_stride);
+    void* s = stream_of(v[5], dev);
+    c10::DeviceGuard guard(dev);
+    return mega_moe_act_backward(&p, ptr(x), ptr(d_out), static_cast<const int32_t*>(ptr(num_valid)), ptr(d_x), s);
+  });
+}
+
 PyMethodDef methods[] = {
     {"norm_quant", (PyCFunction)(void (*)(void))norm_quant, METH_FASTCALL, nullptr},
     {"gate_logits", (PyCFunction)(void (*)(void))gate_logits, METH_FASTCALL, nullptr},
     {"gate_topk", (PyCFunction)(void (*)(void))gate_topk, METH_FASTCALL, nullptr},
+    {"sort_tokens", (PyCFunction)(void (*)(void))sort_tokens, METH_FASTCALL, nullptr},
+    {"unsort_tokens", (PyCFunction)(void (*)(void))unsort_tokens, METH_FASTCALL, nullptr},
+    {"unsort_backward", (PyCFunction)(void (*)(void))unsort_backward, METH_FASTCALL, nullptr},
+    {"block_product", (PyCFunction)(void (*)(void))block_product, METH_FASTCALL, nullptr},
+    {"act_quant", (PyCFunction)(void (*)(void))act_quant, METH_FASTCALL, nullptr},
+    {"act_backward", (PyCFunction)(void (*)(void))act_backward, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 

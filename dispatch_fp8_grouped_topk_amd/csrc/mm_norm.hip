@@ -19,50 +19,10 @@
 // code jumps where amax/448 passes a power of two: where the float32 value lies within 16 units in
 // the last place of one (its error is at most 5: one rounding each of |h w|, r and two products, up
 // to two units each just above a power of two), the code is decided again in float64.
-#include "mm_front.h"
+#include "mm_rows.h"
 
 namespace mm {
 namespace {
-
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-
-// Two floats -> two BF16, round to nearest even, NaN kept.
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const bf16x2 v = __builtin_convertvector((f32x2){lo, hi}, bf16x2);
-  return __builtin_bit_cast(uint32_t, v);
-}
-
-// Largest of the bits of |v| over 4 neighbouring lanes / the 16 lanes of a row.  As unsigned
-// integers magnitudes order as their values do, with infinity and NaN above every number.
-__device__ __forceinline__ uint32_t max4(uint32_t m) {
-  m = max(m, dpp<kXor1>(m));
-  return max(m, dpp<kXor2>(m));
-}
-__device__ __forceinline__ uint32_t max16(uint32_t m) {
-  m = max4(m);
-  m = max(m, dpp<kHalfMirror>(m));
-  return max(m, dpp<kMirror>(m));
-}
-
-constexpr uint32_t kInfBits = 0x7F800000u;
-
-__device__ __forceinline__ uint32_t mag(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
-
-__device__ __forceinline__ uint4 pack_bf16x8(const float (&v)[8]) {
-  return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-}
-
-template <bool kF32>
-__device__ __forceinline__ void store8(void* base, size_t elem, const float (&v)[8]) {
-  if constexpr (kF32) {
-    float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + elem);
-    p[0] = make_float4(v[0], v[1], v[2], v[3]);
-    p[1] = make_float4(v[4], v[5], v[6], v[7]);
-  } else {
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + elem) = pack_bf16x8(v);
-  }
-}
 
 // 1 / sqrt(m) for a positive float64: the hardware's estimate and two Newton steps.  A mean that is
 // not finite gives NaN.
@@ -72,42 +32,6 @@ __device__ __forceinline__ double rsqrt64(double m) {
   y = y * (1.5 - 0.5 * m * y * y);
   return m < __builtin_inf() ? y : __builtin_nan("");
 }
-
-// The UE8M0 code of the smallest power of two >= r, for a finite r >= 0 in float64.
-__device__ __forceinline__ uint32_t ue8m0_ceil64(double r) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, r);
-  const int e = (int)(u >> 52) - 1023 + 127 + ((u & 0xFFFFFFFFFFFFFull) ? 1 : 0);
-  return (uint32_t)min(max(e, 0), 254);
-}
-
-// Eight values as loaded.
-template <bool kF32>
-struct Raw {
-  uint4 v[kF32 ? 2 : 1];
-  __device__ __forceinline__ void load(const void* base, size_t elem) {
-    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(base) + elem * (kF32 ? 4 : 2));
-    v[0] = p[0];
-    if constexpr (kF32) v[1] = p[1];
-  }
-  __device__ __forceinline__ void values(float (&f)[8]) const {
-    if constexpr (kF32) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        f[4 * i] = __uint_as_float(v[i].x);
-        f[4 * i + 1] = __uint_as_float(v[i].y);
-        f[4 * i + 2] = __uint_as_float(v[i].z);
-        f[4 * i + 3] = __uint_as_float(v[i].w);
-      }
-    } else {
-      const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-      }
-    }
-  }
-};
 
 template <bool kXF32, bool kWF32, bool kPer32, int kNC>
 __global__ __launch_bounds__(1024) void k_norm_quant(NormArgs a) {

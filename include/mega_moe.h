@@ -312,7 +312,11 @@ int mega_moe_diag_mfma_block_sums(int fmt, const void* a, const void* b, const v
  * Those of the norm and of the choice of experts do not depend on the row's place in the batch
  * either (num_tokens may change the last bits of topk_w); those of the gate product as stated there.
  * Errors: INVALID_ARG, NULL_POINTER, MISALIGNED, UNSUPPORTED_DEVICE, HIP. */
-typedef enum { MEGA_MOE_DTYPE_BF16 = 0, MEGA_MOE_DTYPE_F32 = 1 } mega_moe_dtype;
+typedef enum {
+  MEGA_MOE_DTYPE_BF16 = 0,
+  MEGA_MOE_DTYPE_F32 = 1,
+  MEGA_MOE_DTYPE_E4M3 = 2   /* mega_moe_sort_tokens only */
+} mega_moe_dtype;
 typedef enum { MEGA_MOE_SCORE_SOFTMAX = 0, MEGA_MOE_SCORE_SIGMOID = 1 } mega_moe_score;
 
 typedef struct {
@@ -416,6 +420,166 @@ typedef struct {
  *              not looked at */
 int mega_moe_gate_topk(const mega_moe_topk_problem* p, const void* logits, const float* bias,
                        const int32_t* num_valid, int32_t* topk_idx, float* topk_w, void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * The layer in parts: what mega_moe_forward does in one call, as operators of its own, for what the
+ * one call does not do: other activations or adapters between the two products, dense 8-bit layers,
+ * and the gradients of what stands between the router and the experts (the experts' 8-bit weights
+ * themselves are held fixed).  In the order of their use:
+ *
+ *   mega_moe_sort_tokens     each routed pair's row to its expert's place, with the plan
+ *   mega_moe_block_product   y = x w^T in 8 bits with a scale for each block of 128, by expert or dense
+ *   mega_moe_act_quant       activation, 8-bit rows with the recipe's scales: the next product's x
+ *   mega_moe_unsort_tokens   weighted sum of each token's expert rows
+ *
+ * and backwards:
+ *
+ *   mega_moe_unsort_backward   gradients of the rows and of the weights
+ *   mega_moe_act_backward      gradient of the activation
+ *   mega_moe_block_product     gradient of x: the product of the 8-bit gradient (mega_moe_act_quant with
+ *                              MEGA_MOE_ACT_NONE) with the transposed weights
+ *   mega_moe_unsort_tokens     gradient of the sort: without weights
+ *
+ * As for the operators in front of the layer, they allocate and synchronise nothing, keep nothing
+ * between calls, can be captured into a HIP graph, run on `stream`, whose device has to be the current
+ * one, and validate their arguments synchronously, before the device is touched.  Pointers are device
+ * memory, 16-byte aligned unless stated.  An output overlaps no input and no other output, from its
+ * first element to its last, except where stated (INVALID_ARG).  The same call gives the same results
+ * bit for bit.
+ * Errors: INVALID_ARG, NULL_POINTER, MISALIGNED, WORKSPACE_TOO_SMALL, UNSUPPORTED_DEVICE, HIP. */
+typedef struct {
+  int64_t num_tokens;    /* T >= 0, T * topk below 2^30 */
+  int32_t hidden;        /* H in (0, 16384], multiple of 128 */
+  int32_t num_experts;   /* E in [1, 8192] */
+  int32_t topk;          /* k in [1, 64] */
+  int32_t dtype;         /* mega_moe_dtype of x and rows */
+  int32_t recipe;        /* mega_moe_recipe: which scales go with rows in MEGA_MOE_DTYPE_E4M3 */
+  uint32_t flags;        /* 0 */
+  int64_t x_stride;      /* elements from one row of x to the next: 0 (= H), or >= H in whole 16-byte steps,
+                            < 2^40 */
+} mega_moe_sort_problem;
+
+/* Bytes of workspace a mega_moe_sort_tokens call of this problem needs; 0 for small batches.
+   Errors: NULL_POINTER, INVALID_ARG; *bytes_out is written only on success. */
+int mega_moe_sort_workspace_size(const mega_moe_sort_problem* p, size_t* bytes_out);
+
+/* Tokens sorted by expert.  The pairs t*k + j with an id in [0, E) take places in the order of their
+ * ids, pairs of one expert in their own order; other ids have no place.  n of them have one:
+ *   expert_offset[e] = pairs with an id below e   (expert_offset[E] = n)
+ *   pool_src[r] = the pair at place r;  pair_pos[t*k + j] = its place, or -1
+ *   rows[r] = x[pool_src[r] / k],  rows_sf[r] = x_sf[pool_src[r] / k]
+ * the dispatch of mega_moe_forward (its views have the same names).  Places from n on are left as they
+ * were in pool_src, rows and rows_sf.  With num_tokens == 0, expert_offset is zeroed and nothing else is
+ * looked at.  Its gradient: mega_moe_unsort_tokens of the rows' gradients without weights.
+ *   x         [T, H] dtype, rows x_stride apart, or NULL with rows NULL: the plan alone
+ *   x_sf      f32 [T, H/128] | u8 [T, H/32] (per-32 recipes) with MEGA_MOE_DTYPE_E4M3, otherwise NULL
+ *   topk_idx  i32 [T, k]
+ *   rows      [T*k, H] dtype;  rows_sf [T*k, H/128] | [T*k, H/32] as x_sf
+ *   pool_src  i32 [T*k];  pair_pos i32 [T, k];  expert_offset i32 [E + 1]
+ *   workspace of mega_moe_sort_workspace_size() bytes (NULL where that is 0), used by no other call at the
+ *             same time; it needs no initialisation */
+int mega_moe_sort_tokens(const mega_moe_sort_problem* p, const void* x, const void* x_sf, const int32_t* topk_idx,
+                         void* rows, void* rows_sf, int32_t* pool_src, int32_t* pair_pos, int32_t* expert_offset,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+typedef struct {
+  int64_t num_tokens;    /* T >= 0, T * topk below 2^30 */
+  int64_t num_rows;      /* rows of `rows` and d_rows: 0 (= T * topk), or up to 2^30 */
+  int32_t hidden;        /* H in (0, 16384], multiple of 128 */
+  int32_t topk;          /* k in [1, 64] */
+  int32_t dtype;         /* BF16 or F32: rows and y (dy, d_rows) */
+  uint32_t flags;        /* 0 */
+  int64_t stride;        /* elements from one row of y (dy) to the next: 0 (= H), or >= H in whole 16-byte
+                            steps, < 2^40 */
+} mega_moe_unsort_problem;
+
+/* Expert rows back in token order:
+ *   y[t] = sum_j topk_w[t, j] * rows[pair_pos[t, j]]
+ * in float32, ascending j, rounded once.  Pairs whose pair_pos is not in [0, num_rows) contribute
+ * nothing (their weight and any row without a pair are not looked at); a token without pairs gives 0.
+ *   rows [num_rows, H] dtype;  pair_pos i32 [T, k];  topk_w f32 [T, k], or NULL: 1
+ *   y    [T, H] dtype, rows `stride` apart */
+int mega_moe_unsort_tokens(const mega_moe_unsort_problem* p, const void* rows, const int32_t* pair_pos,
+                           const float* topk_w, void* y, void* stream);
+
+/* Gradients of mega_moe_unsort_tokens, for each pair with a place r = pair_pos[t, j]:
+ *   d_rows[r] = topk_w[t, j] * dy[t]               (rounded once)
+ *   d_w[t, j] = sum_h rows[r, h] * dy[t, h]        (sums of 8 columns in float32, joined in float64)
+ * d_w of other pairs is 0; places without a pair are left as they were in d_rows.  No two pairs share a place
+ * (as mega_moe_sort_tokens makes them): of two that do, either may be left in d_rows.
+ *   dy   [T, H] dtype, rows `stride` apart;  rows as above, may be NULL where d_w is
+ *   d_rows [num_rows, H] dtype or NULL, may be `rows` itself;  d_w f32 [T, k] or NULL; not both NULL */
+int mega_moe_unsort_backward(const mega_moe_unsort_problem* p, const void* dy, const void* rows,
+                             const int32_t* pair_pos, const float* topk_w, void* d_rows, float* d_w, void* stream);
+
+typedef struct {
+  int64_t num_rows;      /* M in [0, 2^30) */
+  int32_t n;             /* N in (0, 2^20], multiple of 8: rows of each group's weights */
+  int32_t k;             /* K in (0, 16384], multiple of 128 */
+  int32_t num_groups;    /* G in [1, 8192] */
+  uint32_t flags;        /* 0 */
+  int64_t x_stride;      /* elements from one row of x to the next: 0 (= K), or >= K and a multiple of 16,
+                            at most 2^22 */
+  int64_t y_stride;      /* the same for y: 0 (= N), or >= N and a multiple of 8, < 2^40 */
+} mega_moe_product_problem;
+
+/* Matrix product in 8 bits with a scale for each block of 128, of each group's rows with its weights:
+ *   y[m, n] = bf16( sum_b x_sf[m, b] * w_sf[g, n / 128, b] * sum_{k in block b} x[m, k] * w[g, n, k] )
+ * for group_offset[g] <= m < group_offset[g + 1]: the scales and weights of MEGA_MOE_RECIPE_FP8_B128.
+ * Block sums are the matrix cores' (see mega_moe_diag_mfma_block_sums), scaled and added up in float32.
+ * Rows outside the groups are left as they were in y and not looked at in x.  A row's values depend on its own
+ * inputs and its group's weights alone, but the order of their sums, and so their last bits, goes by the problem's
+ * sizes and by the row's place in its group.
+ *   x  u8 (E4M3) [M, K], rows x_stride apart;  x_sf f32 [M, K/128]
+ *   w  u8 (E4M3) [G, N, K];  w_sf f32 [G, ceil(N/128), K/128]
+ *   group_offset  i32 [G + 1] in device memory (4-byte aligned), ascending within [0, M] (expert_offset of
+ *                 mega_moe_sort_tokens; other values are taken as the nearest that are), or NULL with one group:
+ *                 every row
+ *   y  bf16 [M, N], rows y_stride apart
+ * The gradient of x is the same product with y's gradient in 8 bits and the weights transposed,
+ * w^T [G, K, N] with w_sf transposed alike, where N is a multiple of 128. */
+int mega_moe_block_product(const mega_moe_product_problem* p, const void* x, const float* x_sf, const void* w,
+                           const float* w_sf, const int32_t* group_offset, void* y, void* stream);
+
+typedef enum { MEGA_MOE_ACT_NONE = 0, MEGA_MOE_ACT_SWIGLU = 1 } mega_moe_act;
+
+typedef struct {
+  int64_t num_rows;      /* M in [0, 2^30) */
+  int32_t width;         /* I in (0, 16384], multiple of 128: columns of the result */
+  int32_t act;           /* mega_moe_act */
+  int32_t recipe;        /* mega_moe_recipe: which scales q_sf holds */
+  int32_t x_dtype;       /* BF16 or F32: x (d_out, d_x) */
+  float swiglu_clamp;    /* as in mega_moe_problem: 0 or +inf: none; only with MEGA_MOE_ACT_SWIGLU */
+  uint32_t flags;        /* 0 or MEGA_MOE_FLAG_CLAMP_INPUTS */
+  int64_t x_stride;      /* elements from one row of x (d_x) to the next: 0 (= its columns), or more in whole
+                            16-byte steps, < 2^40 */
+} mega_moe_act_problem;
+
+/* Activation and quantisation of each row:
+ *   v = x                          (MEGA_MOE_ACT_NONE, x [M, I])
+ *   v = clamp(silu(g) * u)         (MEGA_MOE_ACT_SWIGLU, x [M, 2I]: g the first I columns, u the others; with
+ *                                   MEGA_MOE_FLAG_CLAMP_INPUTS the clamp is on g and u instead)
+ *   q, q_sf = v in 8 bits with the recipe's scales, out = bf16(v)
+ * in float32 (silu with the hardware's exponential and reciprocal, a few ulp), each output rounded once; scales
+ * and codes as mega_moe_norm_quant makes them, a UE8M0 code decided as if in float64.  A group with a v that is
+ * not finite has NaN q and q_sf; others are not affected.
+ *   x          [M, I] | [M, 2I] x_dtype, rows x_stride apart
+ *   num_valid  i32 [1] in device memory (4-byte aligned) or NULL: rows from *num_valid on are not looked at, and
+ *              left as they were in the outputs (expert_offset + E of mega_moe_sort_tokens, say)
+ *   q          u8 [M, I], q_sf f32 [M, I/128] | u8 [M, I/32] (per-32 recipes): both or neither
+ *   out        bf16 [M, I] or NULL; out, or q and q_sf, must be given (INVALID_ARG otherwise) */
+int mega_moe_act_quant(const mega_moe_act_problem* p, const void* x, const int32_t* num_valid, void* q, void* q_sf,
+                       void* out, void* stream);
+
+/* Gradient of the SwiGLU (INVALID_ARG with another activation; the recipe is not looked at, the rounding to
+ * 8 bits passes gradients on as they are), with s = 1 / (1 + exp(-g)):
+ *   d_g = d_out * u * s * (1 + g (1 - s)),  d_u = d_out * g * s
+ * both 0 where silu(g) * u lies outside [-c, c] (decided as in float64), or with MEGA_MOE_FLAG_CLAMP_INPUTS each
+ * where its own input does (g and u in the formulas are then the clamped ones); in float32, rounded once.
+ *   x [M, 2I] x_dtype, rows x_stride apart;  d_out [M, I] x_dtype;  num_valid as above
+ *   d_x [M, 2I] x_dtype, rows x_stride apart; may be x itself */
+int mega_moe_act_backward(const mega_moe_act_problem* p, const void* x, const void* d_out, const int32_t* num_valid,
+                          void* d_x, void* stream);
 
 /* Static text for a status code. */
 const char* mega_moe_strerror(int status);
