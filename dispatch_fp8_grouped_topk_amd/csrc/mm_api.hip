@@ -831,8 +831,6 @@ MM_EXPORT int mega_moe_block_product(const mega_moe_product_problem* p, const vo
   a.N = (int)N;
   a.K = (int)K;
   a.G = (int)G;
-  a.cus = device_cus();
-  if (!a.cus) return MEGA_MOE_ERR_HIP;
   return mm::launch_product(a, static_cast<hipStream_t>(stream)) == hipSuccess ? MEGA_MOE_OK : MEGA_MOE_ERR_HIP;
 }
 

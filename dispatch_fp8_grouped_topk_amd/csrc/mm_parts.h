@@ -62,7 +62,6 @@ struct ProductArgs {
   uint16_t* y;               // [M, N], rows y_stride apart
   long x_stride, y_stride;
   int M, N, K, G;
-  int cus;                   // compute units of the device
 };
 
 hipError_t launch_product(const ProductArgs& a, hipStream_t s);

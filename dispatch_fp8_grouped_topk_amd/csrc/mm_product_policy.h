@@ -1,0 +1,55 @@
+// Which kernel and tile the 8-bit product takes, by sizes.  No HIP headers: a plain C++ compiler can check it on the CPU.
+#pragma once
+
+#include <stdint.h>
+
+namespace mm {
+
+// The instances built: a workgroup's weight rows and rows of x, and what its time goes by, fitted (us) to the times of
+// every instance at 72 dense sizes (M 1 to 8192; N, K of 512 x 512, 512 x 7168, 2048 x 2048, 4096 x 7168, 7168 x 2048,
+// 8192 x 512) to within 7 to 16% in the mean: per round of 256 workgroups a fixed part and one for each of the K/128 blocks.
+// The first kProductSplit share K among a workgroup's waves (k_product_split, block time of all its waves together), the
+// others share the tile (k_product_large).  The smallest sum wins; over those sizes and 30 more by 4 to 256 groups the
+// choice takes 2.7% longer than the best instance in the mean.  Both sides of some borders (us, K 7168, N 4096):
+// M 16 {16, 16} 7.7, {32, 32} 8.5; M 128 {64, 32} 12.5, {64, 64} 17.4; M 256 {64, 64} 18.2, {128, 64} 24.9; M 512 {128, 64}
+// 28.1, {64, 64} 34.4; M 1024 {128, 128} 39.4, {128, 64} 52.3; M 2048 {256, 128} 60.4, {256, 256} 85.4; M 4096 {256, 256} 103,
+// {256, 128} 118.
+struct ProductTile {
+  int n, m;
+  float fixed, block;        // us a round, us a round and block
+  int most_blocks;           // of K that its LDS holds the scales of
+};
+constexpr ProductTile kProductTiles[] = {
+    {16, 16, 1.9f, .049f, 128}, {16, 32, 1.75f, .073f, 128}, {32, 32, 1.8f, .101f, 128}, {64, 32, 2.3f, .133f, 128},
+    {64, 64, 3.0f, .203f, 112}, {128, 64, 1.75f, .387f, 128}, {128, 128, 2.5f, .498f, 128}, {256, 64, 2.5f, .518f, 128},
+    {256, 128, 3.3f, .724f, 128}, {256, 256, 3.9f, 1.27f, 128}};
+constexpr int kProductCount = sizeof(kProductTiles) / sizeof(kProductTiles[0]), kProductSplit = 5;
+
+// Most workgroups of a launch, whose threads are counted in 32 bits; the largest tile never has more (y alone would pass
+// 2^39 bytes, or there are at most 2^22 of its tiles).
+constexpr int64_t kProductGroups = 1 << 22;
+
+constexpr int64_t up_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Workgroups that have rows: the rows of G groups are not known here and taken as uneven, each group's last tile as
+// about half full.
+constexpr int64_t product_workgroups(const ProductTile& t, int64_t M, int64_t N, int64_t G) {
+  const int64_t active = G < M ? G : M;
+  const int64_t tiles = G == 1 ? up_div(M, t.m) : active + up_div(M * M, (M + active * t.m) * t.m);
+  return up_div(N, t.n) * tiles;
+}
+
+constexpr int product_variant(int64_t M, int64_t N, int64_t K, int64_t G) {
+  int best = kProductCount - 1;
+  float least = 0.f;
+  for (int i = 0; i < kProductCount; ++i) {
+    const ProductTile& t = kProductTiles[i];
+    const int64_t w = product_workgroups(t, M, N, G), most = up_div(N, t.n) * (up_div(M, t.m) + G);
+    if (K / 128 > t.most_blocks || (i + 1 < kProductCount && most > kProductGroups)) continue;
+    const float cost = (float)up_div(w, 256) * (t.fixed + (float)(K / 128) * t.block);
+    if (least == 0.f || cost < least) best = i, least = cost;
+  }
+  return best;
+}
+
+}  // namespace mm
