@@ -155,8 +155,8 @@ __global__ __launch_bounds__(256) void k_act_backward(ActArgs a) {
       g[n] = keep_g ? d[n] * u[n] * s.s * (1.0f + g[n] * s.rest) : 0.f;
       u[n] = keep_u ? du : 0.f;
     }
-    store8<kF32>(a.d_x, at, g);
-    store8<kF32>(a.d_x, at + a.I, u);
+    store8_nt<kF32>(a.d_x, at, g);
+    store8_nt<kF32>(a.d_x, at + a.I, u);
   }
 }
 

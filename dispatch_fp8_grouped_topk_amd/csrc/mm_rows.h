@@ -36,6 +36,12 @@ __device__ __forceinline__ uint4 pack_bf16x8(const float (&v)[8]) {
   return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
 }
 
+// Stores past the caches: rows that are written once, to places all over the memory or in larger amounts than the caches
+// hold.
+__device__ __forceinline__ void store16_nt(void* to, const uint4& v) {
+  __builtin_nontemporal_store(v4i{(int)v.x, (int)v.y, (int)v.z, (int)v.w}, static_cast<v4i*>(to));
+}
+
 template <bool kF32>
 __device__ __forceinline__ void store8(void* base, size_t elem, const float (&v)[8]) {
   if constexpr (kF32) {
@@ -52,6 +58,17 @@ __device__ __forceinline__ uint32_t ue8m0_ceil64(double r) {
   const uint64_t u = __builtin_bit_cast(uint64_t, r);
   const int e = (int)(u >> 52) - 1023 + 127 + ((u & 0xFFFFFFFFFFFFFull) ? 1 : 0);
   return (uint32_t)min(max(e, 0), 254);
+}
+
+template <bool kF32>
+__device__ __forceinline__ void store8_nt(void* base, size_t elem, const float (&v)[8]) {
+  if constexpr (kF32) {
+    float* p = static_cast<float*>(base) + elem;
+    store16_nt(p, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])));
+    store16_nt(p + 4, make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])));
+  } else {
+    store16_nt(static_cast<uint16_t*>(base) + elem, pack_bf16x8(v));
+  }
 }
 
 // Eight values as loaded.

@@ -16,18 +16,23 @@ namespace {
 // counting the pairs that sort before each: with key(p) = expert * 4096 + p they are those with a smaller key.  A
 // comparison of 64 pairs is one vector instruction and a count of bits, so 4096 pairs take 16 of them a wave and pair;
 // that is cheaper than a second launch.  The last workgroup makes expert_offset.
-template <bool kMove>
+template <bool kMove, int kIds>
 __global__ __launch_bounds__(256) void k_sort_small(SortArgs a, int parts) {
   extern __shared__ int hist[];                  // [E], the last workgroup
   __shared__ int s_cnt[4][8], s_pos[8], sh[32];
   const int tid = threadIdx.x, wave = tid >> 6;
+  // every id is asked for before anything that waits
+  int ids[kIds];
+#pragma unroll
+  for (int i = 0; i < kIds; ++i) ids[i] = tid + 256 * i < a.P ? a.idx[tid + 256 * i] : -1;
   if ((int)blockIdx.x == a.T * parts) {
     for (int e = tid; e < a.E; e += 256) hist[e] = 0;
     __syncthreads();
-    for (int p = tid; p < a.P; p += 256) {
-      const int e = a.idx[p];
+    const auto count = [&](int e) {
       if (e >= 0 && e < a.E) atomicAdd(&hist[e], 1);
-    }
+    };
+#pragma unroll
+    for (int i = 0; i < kIds; ++i) count(ids[i]);
     __syncthreads();
     const int per = (a.E + 255) / 256, lo = min(tid * per, a.E), hi = min(lo + per, a.E);
     int sum = 0;
@@ -56,29 +61,36 @@ __global__ __launch_bounds__(256) void k_sort_small(SortArgs a, int parts) {
       if (c < c_hi) v[i] = from[c];
     }
   }
+  uint32_t word = 0;
+  const bool scales = kMove && a.x_sf && part == 0 && tid < a.sf_words;
+  if (scales) word = a.x_sf[(size_t)t * a.sf_words + tid];
   for (int j0 = 0; j0 < a.k; j0 += 8) {
-    uint32_t key[8];
+    uint32_t key[8], valid = 0;
     int cnt[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int e = j0 + j < a.k ? a.idx[t * a.k + j0 + j] : -1;
-      key[j] = e >= 0 && e < a.E ? (uint32_t)(e * kSortSmallPairs + t * a.k + j0 + j) : 0u;
+      const bool in = e >= 0 && e < a.E;
+      key[j] = in ? (uint32_t)(e * kSortSmallPairs + t * a.k + j0 + j) : 0u;
+      valid |= (uint32_t)in << j;
       cnt[j] = 0;
     }
-    for (int p0 = 0; p0 < a.P; p0 += 256) {
-      const int p = p0 + tid, e = p < a.P ? a.idx[p] : -1;
+    const auto compare = [&](int p, int e) {
       const uint32_t mine = e >= 0 && e < a.E ? (uint32_t)(e * kSortSmallPairs + p) : ~0u;
 #pragma unroll
       for (int j = 0; j < 8; ++j) cnt[j] += __popcll(__ballot(mine < key[j]));
-    }
+    };
+#pragma unroll
+    for (int i = 0; i < kIds; ++i)
+      if (256 * i < a.P) compare(tid + 256 * i, ids[i]);
     if ((tid & 63) == 0) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) s_cnt[wave][j] = cnt[j];
     }
     __syncthreads();
     if (tid < 8 && j0 + tid < a.k) {
-      const int p = t * a.k + j0 + tid, e = a.idx[p];
-      const int at = e >= 0 && e < a.E ? s_cnt[0][tid] + s_cnt[1][tid] + s_cnt[2][tid] + s_cnt[3][tid] : -1;
+      const int p = t * a.k + j0 + tid;
+      const int at = (valid >> tid) & 1 ? s_cnt[0][tid] + s_cnt[1][tid] + s_cnt[2][tid] + s_cnt[3][tid] : -1;
       s_pos[tid] = at;
       if (part == 0) {
         a.pos[p] = at;
@@ -102,8 +114,7 @@ __global__ __launch_bounds__(256) void k_sort_small(SortArgs a, int parts) {
         if (c < c_hi) put(c, v[i]);
       }
       for (int c = c_lo + tid + 256 * kAhead; c < c_hi; c += 256) put(c, from[c]);
-      if (a.x_sf && part == 0 && tid < a.sf_words) {
-        const uint32_t word = a.x_sf[(size_t)t * a.sf_words + tid];
+      if (scales) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           if (at[j] >= 0) a.rows_sf[(size_t)at[j] * a.sf_words + tid] = word;
@@ -223,7 +234,7 @@ __global__ __launch_bounds__(256) void k_sort_move(SortArgs a) {
           uint4* to = reinterpret_cast<uint4*>(static_cast<char*>(a.rows) + (size_t)r * a.row_bytes);
 #pragma unroll
           for (int i = 0; i < kPieces; ++i)
-            if (c0 + 64 * i + lane < chunks) to[c0 + 64 * i + lane] = v[i];
+            if (c0 + 64 * i + lane < chunks) store16_nt(to + c0 + 64 * i + lane, v[i]);
         }
       }
       if (a.x_sf) {
@@ -237,6 +248,13 @@ __global__ __launch_bounds__(256) void k_sort_move(SortArgs a) {
       }
     }
   }
+}
+
+// kIds: ids a thread holds.  Fewer of them are less code to fetch, which is a part of what a single token takes.
+template <int kIds>
+void launch_small(const SortArgs& a, dim3 grid, int parts, size_t lds, hipStream_t s) {
+  if (a.x) hipLaunchKernelGGL((k_sort_small<true, kIds>), grid, dim3(256), lds, s, a, parts);
+  else hipLaunchKernelGGL((k_sort_small<false, kIds>), grid, dim3(256), lds, s, a, parts);
 }
 
 __global__ __launch_bounds__(256) void k_sort_empty(int32_t* offset, int n) {
@@ -256,8 +274,9 @@ hipError_t launch_sort(const SortArgs& a, hipStream_t s) {
     int parts = 1;
     while (a.x && parts < 4 && (long)a.T * parts * 2 <= 512 && a.row_bytes / 16 > 256 * parts) parts *= 2;
     const dim3 grid((unsigned)(a.T * parts + 1));
-    if (a.x) hipLaunchKernelGGL(k_sort_small<true>, grid, dim3(256), lds, s, a, parts);
-    else hipLaunchKernelGGL(k_sort_small<false>, grid, dim3(256), lds, s, a, parts);
+    if (a.P <= 256) launch_small<1>(a, grid, parts, lds, s);
+    else if (a.P <= 1024) launch_small<4>(a, grid, parts, lds, s);
+    else launch_small<kSortSmallPairs / 256>(a, grid, parts, lds, s);
     return hipGetLastError();
   }
   hipLaunchKernelGGL(k_sort_count, dim3((unsigned)a.NB), dim3(1024), lds, s, a);
@@ -305,15 +324,17 @@ __global__ __launch_bounds__(256) void k_unsort(UnsortArgs a) {
         for (int n = 0; n < 8; ++n) acc[n] = __builtin_fmaf(w[j], f[n], acc[n]);
       }
     }
-    store8<kF32>(a.y, (size_t)t * a.stride + 8 * c, acc);
+    store8_nt<kF32>(a.y, (size_t)t * a.stride + 8 * c, acc);
   }
 }
 
 // ---------------------------------------------------------------------------- back's gradient
-// A workgroup takes a token, its threads eight columns each (two times eight beyond 8192 columns): dy stays in registers,
+// A workgroup takes a token, or for few tokens (kSplit) four of its pairs, its threads eight columns each (two times eight
+// beyond 8192 columns): dy stays in registers,
 // each pair's row is read once for d_w and written once.  Sums of eight products are float32, the rest of d_w's sum is
 // float64: lanes by DPP, waves through LDS in a fixed order.
-template <bool kF32, int kNC>
+constexpr int kAtOnce = 4;                       // pairs whose rows are under way at once
+template <bool kF32, int kNC, bool kSplit>
 __global__ __launch_bounds__(1024) void k_unsort_backward(UnsortArgs a) {
   __shared__ double part[16][kMaxTopk];
   const int chunks = a.H / 8, tid = threadIdx.x, waves = blockDim.x / 64;
@@ -327,8 +348,8 @@ __global__ __launch_bounds__(1024) void k_unsort_backward(UnsortArgs a) {
       raw.load(a.dy, (size_t)t * a.stride + 8 * c);
       raw.values(d[i]);
     }
-    constexpr int kAtOnce = 4;
-    for (int j0 = 0; j0 < a.k; j0 += kAtOnce) {
+    const int j_lo = kSplit ? blockIdx.y * kAtOnce : 0, j_hi = kSplit ? min(j_lo + kAtOnce, a.k) : a.k;
+    for (int j0 = j_lo; j0 < j_hi; j0 += kAtOnce) {
       int at[kAtOnce];
       float w[kAtOnce];
       Raw<kF32> v[kAtOnce][kNC];
@@ -367,7 +388,7 @@ __global__ __launch_bounds__(1024) void k_unsort_backward(UnsortArgs a) {
             float o[8];
 #pragma unroll
             for (int n = 0; n < 8; ++n) o[n] = w[j] * d[i][n];
-            store8<kF32>(a.d_rows, (size_t)at[j] * a.H + 8 * c, o);
+            store8_nt<kF32>(a.d_rows, (size_t)at[j] * a.H + 8 * c, o);
           }
         }
         if (a.d_w) {
@@ -378,7 +399,7 @@ __global__ __launch_bounds__(1024) void k_unsort_backward(UnsortArgs a) {
     }
     if (a.d_w) {
       __syncthreads();
-      if (tid < a.k) {
+      if (tid >= j_lo && tid < j_hi) {
         double dot = 0.0;
         for (int i = 0; i < waves; ++i) dot += part[i][tid];
         a.d_w[t * a.k + tid] = (float)dot;
@@ -388,12 +409,21 @@ __global__ __launch_bounds__(1024) void k_unsort_backward(UnsortArgs a) {
   }
 }
 
+// Below 512 tokens, two workgroups a compute unit, a token's pairs are shared out four by four (k 8, H 7168, us: T 1 7.1 -> 4.8,
+// T 128 9.8 -> 7.5); above, that would only read dy again.
+template <bool kF32, int kNC>
+void launch_backward(const UnsortArgs& a, int threads, hipStream_t s) {
+  if (a.T < 512)
+    hipLaunchKernelGGL((k_unsort_backward<kF32, kNC, true>), dim3(a.T, (a.k + kAtOnce - 1) / kAtOnce), dim3(threads), 0, s, a);
+  else
+    hipLaunchKernelGGL((k_unsort_backward<kF32, kNC, false>), dim3(std::min(a.T, 1 << 20)), dim3(threads), 0, s, a);
+}
+
 template <bool kF32>
 void launch_backward(const UnsortArgs& a, hipStream_t s) {
   const int chunks = a.H / 8, per = chunks <= 1024 ? 1 : 2, threads = ((chunks + per - 1) / per + 63) / 64 * 64;
-  const unsigned grid = (unsigned)std::min(a.T, 1 << 20);
-  if (per == 1) hipLaunchKernelGGL((k_unsort_backward<kF32, 1>), dim3(grid), dim3(threads), 0, s, a);
-  else hipLaunchKernelGGL((k_unsort_backward<kF32, 2>), dim3(grid), dim3(threads), 0, s, a);
+  if (per == 1) launch_backward<kF32, 1>(a, threads, s);
+  else launch_backward<kF32, 2>(a, threads, s);
 }
 
 }  // namespace
