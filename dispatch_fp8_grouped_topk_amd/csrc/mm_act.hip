@@ -4,7 +4,9 @@
 //   UE8M0 code of the smallest power of two that holds amax/448
 //   d_u = d g s,  d_g = d u s (1 + g (1 - s))
 //
-// One pass, eight columns a lane, nothing shared beyond 16 lanes, so the grid is flat over all pieces of all rows.
+// One pass, eight columns a lane, nothing shared beyond 16 lanes, so the grid is flat over all pieces of all rows.  Bound by
+// memory: 65536 x 2048 from BF16 with float scales (665 MB) takes 124 us, 5.3 TB/s; the gradient of 4093 x 1536 in float32
+// (126 MB) 21.3 us, 5.9 TB/s, its stores past the caches (through them 25.3; the 8-bit rows, read next, gain nothing).
 //
 // Numerics: float32 throughout.  With e = exp(-|g|) in (0, 1] and r = 1 / (1 + e), s and 1 - s are r and e r or the other
 // way round: neither overflows or cancels.  The hardware's exponential takes g log2(e), rounded: its relative error is

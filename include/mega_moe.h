@@ -532,9 +532,10 @@ typedef struct {
  * sizes and by the row's place in its group.
  *   x  u8 (E4M3) [M, K], rows x_stride apart;  x_sf f32 [M, K/128]
  *   w  u8 (E4M3) [G, N, K];  w_sf f32 [G, ceil(N/128), K/128]
- *   group_offset  i32 [G + 1] in device memory (4-byte aligned), ascending within [0, M] (expert_offset of
- *                 mega_moe_sort_tokens; other values are taken as the nearest that are), or NULL with one group:
- *                 every row
+ *   group_offset  i32 [G + 1] in device memory (4-byte aligned), ascending (expert_offset of
+ *                 mega_moe_sort_tokens), or NULL with one group: every row.  Values outside [0, M] are taken as the
+ *                 nearest inside.  Where they descend no memory outside the buffers is touched, but a row of two
+ *                 groups gets the values of either, and groups may be left out.
  *   y  bf16 [M, N], rows y_stride apart
  * The gradient of x is the same product with y's gradient in 8 bits and the weights transposed,
  * w^T [G, K, N] with w_sf transposed alike, where N is a multiple of 128. */
@@ -560,8 +561,8 @@ typedef struct {
  *   v = clamp(silu(g) * u)         (MEGA_MOE_ACT_SWIGLU, x [M, 2I]: g the first I columns, u the others; with
  *                                   MEGA_MOE_FLAG_CLAMP_INPUTS the clamp is on g and u instead)
  *   q, q_sf = v in 8 bits with the recipe's scales, out = bf16(v)
- * in float32 (silu with the hardware's exponential and reciprocal, a few ulp), each output rounded once; scales
- * and codes as mega_moe_norm_quant makes them, a UE8M0 code decided as if in float64.  A group with a v that is
+ * in float32 (silu with the hardware's exponential and reciprocal, a few ulp; it may be 0 for g below -87.3, where the
+ * exponential is no normal number), each output rounded once; scales and codes as mega_moe_norm_quant makes them, a UE8M0 code decided as if in float64.  A group with a v that is
  * not finite has NaN q and q_sf; others are not affected.
  *   x          [M, I] | [M, 2I] x_dtype, rows x_stride apart
  *   num_valid  i32 [1] in device memory (4-byte aligned) or NULL: rows from *num_valid on are not looked at, and

@@ -136,9 +136,9 @@ def test_sort_without_any_pair_and_with_one_expert_for_all(T):
         _check_sort(_sort(idx, 9, x), idx, 9, x)
 
 
-@pytest.mark.parametrize("T,E,k", [(300, 50, 4), (5000, 50, 4), (20000, 8192, 60), (1050000, 17, 1)])
+@pytest.mark.parametrize("T,E,k", [(300, 50, 4), (5000, 50, 4), (20000, 8192, 60), (1050000, 17, 1), (4500000, 5, 1)])
 def test_sort_plan_alone(T, E, k):
-    """The last two have more than 1024 blocks of 1024 pairs."""
+    """The last three have more than 1024 blocks of 1024 pairs, the last more tokens than one pass of the workgroups."""
     _say("plan", T, E, k)
     idx = _ids(T, E, k, seed=T)
     _check_sort(_sort(idx, E), idx, E)
@@ -189,7 +189,7 @@ def _unsort_problem(T, H, k, dtype, num_rows=0, stride=0):
 
 BACK = [(1, 7168, 256, 8, 0, 0.0), (1, 128, 1, 1, 0, 0.0), (2, 16384, 9, 64, 8, 0.2), (37, 384, 7, 5, 24, 0.3),
         (128, 7168, 256, 8, 0, 0.0), (513, 1152, 33, 9, 0, 0.5), (70, 8192, 16, 12, 16, 0.1), (33, 8320, 16, 17, 0, 0.1),
-        (2000, 128, 4, 3, 0, 0.9)]
+        (2000, 128, 4, 3, 0, 0.9), (511, 256, 8, 6, 0, 0.1), (512, 256, 8, 6, 8, 0.1), (600, 8320, 8, 3, 8, 0.1)]
 
 
 @pytest.mark.parametrize("weights", [True, False])
@@ -272,6 +272,36 @@ def test_back_past_32_bits():
     want = (taken.double() * dy.double()[:, None]).sum(2)
     mag = (taken.double() * dy.double()[:, None]).abs().sum(2)
     assert ((d_w.double() - want).abs() <= 8 * 2.0 ** -24 * mag + 2.0 ** -23 * want.abs()).all()
+
+
+def test_back_of_more_rows_than_one_pass_of_the_workgroups():
+    T, H = 131200, 16384
+    rows = torch.empty(T, H, dtype=torch.bfloat16, device="cuda").normal_()
+    pos = torch.randperm(T, device="cuda").to(torch.int32).view(T, 1)
+    y = torch.empty_like(rows)
+    mm.mega_moe_unsort_tokens(_unsort_problem(T, H, 1, torch.bfloat16), rows, pos, y)
+    for lo in range(0, T, 16384):
+        assert torch.equal(y[lo:lo + 16384], rows[pos[lo:lo + 16384, 0].long()])
+
+
+@pytest.mark.parametrize("T", [40, 600])
+def test_a_captured_sort_with_other_ids_at_each_replay(T):
+    """Both the one launch and the three; ids, the number of pairs and the rows change."""
+    E, k, H = 20, 8, 256
+    idx, (x, _) = _ids(T, E, k, seed=1), _row_values(T, H, "bf16", 0, 1)
+    out = _sort(idx, E, x)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        _sort(idx, E, x, out=out)
+    for seed in range(2, 6):
+        idx.copy_(_ids(T, E, k, masked=0.2 * (seed - 2), seed=seed))
+        x.copy_(_row_values(T, H, "bf16", 0, seed)[0])
+        for name in ("src", "pos", "offset", "rows", "ws"):
+            out[name].view(torch.uint8).fill_(FILL)
+        graph.replay()
+        torch.cuda.synchronize()
+        _check_sort(out, idx, E, x)
 
 
 @pytest.mark.parametrize("T", [200, 1500])
@@ -396,6 +426,17 @@ def test_product_takes_offsets_out_of_range_as_the_nearest_that_are():
     args = _product_inputs(M, 128, 256, G, 10)
     offset = torch.tensor([-5, 20, 30, 90, 2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1], dtype=torch.int32, device="cuda")
     _check_product(_product(*args, offset=offset), *args, offset)
+
+
+def test_product_of_descending_offsets_stays_within_its_buffers():
+    """Rows of one group alone are right, rows behind every group as they were."""
+    M, G = 120, 4
+    x, x_sf, w, w_sf = _product_inputs(M, 264, 256, G, 11)
+    offset = torch.tensor([0, 50, 20, 100, 90], dtype=torch.int32, device="cuda")
+    y = _product(x, x_sf, w, w_sf, offset)
+    for g, lo, hi in ((0, 0, 20), (2, 50, 100)):
+        _check_product(y[lo:hi], x[lo:hi], x_sf[lo:hi], w[g:g + 1], w_sf[g:g + 1])
+    assert (_bytes(y[100:]) == FILL).all()
 
 
 @pytest.mark.parametrize("M", [1, 40, 300])
@@ -555,6 +596,26 @@ def test_activation_leaves_rows_behind_the_last_valid_one(valid):
     mm.mega_moe_act_backward(mm.ActProblem.make(M, I), x, d, d_x, num_valid=num)
     assert n == M or (_bytes(d_x[n:]) == FILL).all()
     assert torch.isfinite(d_x[:n]).all()
+
+
+def test_activation_of_more_rows_than_one_pass_of_the_workgroups():
+    """More than 2^31 values; the last rows against the oracle, the valid ones end among them."""
+    M, I, n = 131200, 16384, 131190
+    x = torch.empty(M, 2 * I, dtype=torch.bfloat16, device="cuda").normal_()
+    num = torch.tensor([n], dtype=torch.int32, device="cuda")
+    got = _act(x, I, recipe=2, num_valid=num)
+    for rows in (slice(0, 3), slice(n - 3, n)):
+        _check_act(got, x, I, "swiglu", 2, 0.0, False, rows=rows)
+    for t in got.values():
+        assert (_bytes(t[n:]) == FILL).all()
+    del got
+    d = torch.empty(M, I, dtype=torch.bfloat16, device="cuda").normal_()
+    before = x[n - 3:].clone()
+    mm.mega_moe_act_backward(mm.ActProblem.make(M, I), x, d, x, num_valid=num)         # in place
+    ref, mag = parts.act_backward(_f64(before[:3]), _f64(d[n - 3:n]))
+    eps = 2 * np.concatenate([_act_eps(before[:3], I, "swiglu")] * 2, axis=1)
+    assert (np.abs(_f64(x[n - 3:n]) - ref) <= eps * mag * 1.01 + 2.0 ** -8 * np.abs(ref) + TINY[torch.bfloat16]).all()
+    assert torch.equal(x[n:], before[3:])
 
 
 @pytest.mark.parametrize("steps", [0, 1, 3, 60, 127, 129])
