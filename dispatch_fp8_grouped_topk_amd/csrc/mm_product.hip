@@ -30,12 +30,15 @@ __device__ __forceinline__ void group_rows(const ProductArgs& a, int g, int& lo,
 }
 
 // ------------------------------------------------------------------------------- many rows
-// A workgroup takes 64 kWN weight rows x 16 kNG kWM rows of x (kWM = 8 / kWN), its eight waves (two a SIMD) 64 weight rows
-// (wm = wave % kWN) and kNG groups of 16 rows of x (kWM i + wave / kWN) each.  Blocks of 128 columns of both operands, with the rows' scales, go through a
+// A workgroup takes 64 kWN weight rows x 16 kNG kWM rows of x, its eight waves (two a SIMD) 64 weight rows (wm = wave % kWN)
+// and kNG groups of 16 rows of x (kWM i + wave / kWN) each.  With kKS 2 the waves are two sets of four that take every other
+// block, and the second set's sums are added to the first's at the end: half the barriers, for one step more to fill and the
+// hand-over (128 x 64 tiles, us, kKS 1 and 2: 512 x 4096 x 7168 28.1, 25.0; 777 x 2120 x 3712 15.0, 15.5; 2048 x 512 x 512 4.8, 5.1).
+// Blocks of 128 columns of both operands, with the rows' scales, go through a
 // ring in LDS by loads that need no registers; a block's MFMAs run while the next ones are on their way.  16-byte chunk c of
 // a row r sits at c ^ (r / 2 % 8), so that the 16 rows of an operand read fall into different banks.
 //
-// 8192 x 4096 x 7168 in tiles of 256 x 256 takes 221 us, 2170 TFLOP/s, of the 159 us at the 3025 TFLOP/s that a large library
+// 8192 x 4096 x 7168 in tiles of 256 x 256 takes 217 us, 2215 TFLOP/s, of the 159 us at the 3025 TFLOP/s that a large library
 // product with one scale a tensor reaches here.  The matrix units are busy 47% of the cycles at the 2.1 GHz of the loaded chip;
 // a block takes about 4000 cycles for 2048 of MFMAs: the scaling (four multiply-adds an MFMA) runs beside the MFMAs in a
 // register-only loop (4% longer than without), LDS is busy a quarter of the time, and with every workgroup on the same tile,
@@ -104,28 +107,29 @@ __device__ __forceinline__ Tile find_tile(const ProductArgs& a, int t, int* sh, 
   return *found;
 }
 
-template <int kNG, int kWN, int kStages>
+template <int kNG, int kWN, int kKS, int kStages>
 struct LargeLds {
-  static constexpr int kBN = 64 * kWN, kWM = 8 / kWN, kBM = 16 * kNG * kWM;
-  static constexpr int kW = kBN * 128, kX = kBM * 128, kStage = kW + kX + kBM * 16;
+  static constexpr int kBN = 64 * kWN, kWM = 8 / kWN / kKS, kBM = 16 * kNG * kWM;
+  static constexpr int kW = kBN * 128, kX = kBM * 128, kBlock = kW + kX + kBM * 16, kStage = kKS * kBlock;
   uint8_t ring[kStages * kStage];
   float wsc[(kBN + 127) / 128][kMaxKBlocks];
   int sh[32];
   Tile tile;
 };
 
-template <int kNG, int kWN, int kStages>
+template <int kNG, int kWN, int kKS, int kStages>
 __global__ __launch_bounds__(512) void k_product_large(ProductArgs a, int slabs, int tiles) {
-  using L = LargeLds<kNG, kWN, kStages>;
-  constexpr int kBN = L::kBN, kBM = L::kBM, kWM = L::kWM;
-  constexpr int kWLoads = kBN / 64, kXLoads = (kBM + 63) / 64, kSLoads = (kBM + 127) / 128, kLoads = kWLoads + kXLoads + kSLoads;
-  constexpr int kParts = kNG < 4 ? kNG : 4;      // a block's loads go out behind the MFMAs of that many groups of rows
-  constexpr bool kAhead = kNG > 1;               // operands of a block's first group are read in the block before
+  using L = LargeLds<kNG, kWN, kKS, kStages>;
+  constexpr int kBN = L::kBN, kBM = L::kBM, kWM = L::kWM, kGW = 8 / kKS;     // kGW: waves that share a block
+  constexpr int kWLoads = kBN / 8 / kGW, kXLoads = (kBM / 8 + kGW - 1) / kGW, kSLoads = (kBM / 16 + kGW - 1) / kGW,
+                kLoads = kWLoads + kXLoads + kSLoads;
+  constexpr bool kAhead = kNG > 1 && kKS == 1;   // operands of a block's first group are read in the block before
+  constexpr int kParts = !kAhead ? 1 : kNG < 4 ? kNG : 4;   // a block's loads go out behind the MFMAs of that many groups of rows
   static_assert((kStages - 1) * kLoads < 64, "vmcnt holds 6 bits");
   __shared__ __align__(1024) L lds;
   const int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lg = lane >> 4;
-  const int w = __builtin_amdgcn_readfirstlane(tid >> 6), wm = w % kWN, wn = w / kWN;
-  const int KB = a.K / 128;
+  const int w8 = __builtin_amdgcn_readfirstlane(tid >> 6), ks = w8 / kGW, w = w8 % kGW, wm = w % kWN, wn = w / kWN;
+  const int KB = a.K / 128, steps = (KB + kKS - 1) / kKS;
   // each XCD walks a contiguous range of items; an item is (band of 4 tiles, slab, tile of the band)
   const int per_xcd = gridDim.x >> 3, item = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
   if (item >= slabs * tiles) return;
@@ -149,8 +153,8 @@ __global__ __launch_bounds__(512) void k_product_large(ProductArgs a, int slabs,
     const int n = (r & ~63) + 16 * (m >> 2) + 4 * ((r >> 4) & 3) + (m & 3);
     wo[j] = (uint32_t)n * (uint32_t)a.K + 16u * (uint32_t)((lane & 7) ^ ((r >> 1) & 7));
   }
-  const auto x_piece = [&](int j) { return min(w + 8 * j, kBM / 8 - 1); };
-  const auto s_piece = [&](int j) { return min(w + 8 * j, kBM / 16 - 1); };
+  const auto x_piece = [&](int j) { return min(w + kGW * j, kBM / 8 - 1); };
+  const auto s_piece = [&](int j) { return min(w + kGW * j, kBM / 16 - 1); };
 #pragma unroll
   for (int j = 0; j < kXLoads; ++j) {
     const int r = 8 * x_piece(j) + (lane >> 3);
@@ -161,12 +165,17 @@ __global__ __launch_bounds__(512) void k_product_large(ProductArgs a, int slabs,
     const int r = 16 * s_piece(j) + (lane >> 2);
     so[j] = ((uint32_t)min(r, rows - 1) * (uint32_t)KB + (uint32_t)(lane & 3)) * 4u;
   }
-  const auto stage = [&](int slot) { return lds.ring + slot * L::kStage; };
-  // A wave's share of block kb.  Loads past the last block count but fetch nothing: a lane offset of 2^31 lies past any
+  // In the largest tiles the XCDs start at different columns and wrap round, so that they do not all ask for the same columns of
+  // their rows at once (8192 x 4096 x 7168 222 -> 217 us, 8192 x 7168 x 2048 140 -> 129; smaller tiles lose up to 5%).
+  const int rot = kNG == 8 ? (int)(blockIdx.x & 7) * KB / 8 : 0;
+  const auto turned = [&](int kb) { return kNG < 8 || kb + rot < KB ? kb + rot : kb + rot - KB; };
+  const auto stage = [&](int slot) { return lds.ring + slot * L::kStage + ks * L::kBlock; };
+  // A wave's share of its block of step i.  Loads past the last block count but fetch nothing: a lane offset of 2^31 lies past any
   // buffer's end.
-  const auto fetch = [&](int kb, int slot, int part, int parts) {
+  const auto fetch = [&](int step, int slot, int part, int parts) {
     uint8_t* to = stage(slot);
-    const uint32_t past = kb < KB ? 0u : 0x80000000u, k = kb < KB ? (uint32_t)kb : 0u;
+    const int kb = kKS * step + ks;
+    const uint32_t past = kb < KB ? 0u : 0x80000000u, k = kb < KB ? (uint32_t)turned(kb) : 0u;
 #pragma unroll
     for (int i = kLoads * part / parts; i < kLoads * (part + 1) / parts; ++i) {
       const int x = i - kWLoads, f = x - kXLoads;
@@ -217,68 +226,89 @@ __global__ __launch_bounds__(512) void k_product_large(ProductArgs a, int slabs,
     read_first(stage(0));
   }
   int slot = 0;
-  for (int kb = 0; kb < KB; ++kb) {
+  for (int step = 0; step < steps; ++step) {
+    const int kb = kKS * step + ks, at = turned(kb);
     const uint8_t* S = stage(slot);
     const int last = slot == 0 ? kStages - 1 : slot - 1, next = slot + 1 == kStages ? 0 : slot + 1;
     if (!kAhead) {
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       wait_vmcnt<(kStages - 2) * kLoads>();
       pipeline_barrier();                        // the block is in LDS, the one before has been read
-      read_first(S);
     }
-    v4f p[2][4];
-    float sx[kNG];
-    const float cw = wsc[kb];
+    if (kKS == 1 || kb < KB) {                   // no wave is left out of a barrier
+      v4f p[2][4];
+      float sx[kNG];
+      if (!kAhead) read_first(S);
+      const float cw = wsc[at];
 #pragma unroll
-    for (int i = 0; i < kNG; ++i) {
-      v8i Bn = B;
-      if (i + 1 < kNG) Bn = lds_operand(S + xlo, S + xhi, kGroup * (i + 1));
-      if (i == 0) {
+      for (int i = 0; i < kNG; ++i) {
+        v8i Bn = B;
+        if (i + 1 < kNG) Bn = lds_operand(S + xlo, S + xhi, kGroup * (i + 1));
+        if (i == 0) {
 #pragma unroll
-        for (int n = 0; n < kNG; ++n) sx[n] = *reinterpret_cast<const float*>(S + slo + kGroup / 8 * n + 4 * (kb & 3));
-      }
-      if (kAhead && i + 1 == kNG) {
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // this block has been read
-        wait_vmcnt<(kStages - 2) * kLoads>();
-        pipeline_barrier();                      // by every wave, and the next one is in LDS
-      }
-      const float sc = i > 0 ? sx[i - 1] * cw : pend_s;
-#pragma unroll
-      for (int rt = 0; rt < 4; ++rt) {
-        p[i & 1][rt] = mfma_block(A[rt], B);
-        if (i > 0) acc[rt][i - 1] += p[(i - 1) & 1][rt] * sc;
-        else acc[rt][kNG - 1] += pend[rt] * sc;
-      }
-      if (i + 1 < kNG) {
-        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+          for (int n = 0; n < kNG; ++n) sx[n] = *reinterpret_cast<const float*>(S + slo + kGroup / 8 * n + 4 * (at & 3));
+        }
+        if (kAhead && i + 1 == kNG) {
+          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // this block has been read
+          wait_vmcnt<(kStages - 2) * kLoads>();
+          pipeline_barrier();                      // by every wave, and the next one is in LDS
+        }
+        const float sc = i > 0 ? sx[i - 1] * cw : pend_s;
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) {
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-          __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);
+          p[i & 1][rt] = mfma_block(A[rt], B);
+          if (i > 0) acc[rt][i - 1] += p[(i - 1) & 1][rt] * sc;
+          else acc[rt][kNG - 1] += pend[rt] * sc;
         }
-        __builtin_amdgcn_sched_barrier(0);
-        if (i + 1 < kParts) {
-          fetch(kb + kStages - 1, last, i + 1, kParts);
+        if (i + 1 < kNG) {
+          __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+#pragma unroll
+          for (int rt = 0; rt < 4; ++rt) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+          if (i + 1 < kParts) {
+            fetch(step + kStages - 1, last, i + 1, kParts);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+          B = Bn;
+        } else {
+          __builtin_amdgcn_sched_barrier(0);
+          if (kAhead) read_first(stage(next));
+          __builtin_amdgcn_sched_barrier(0);
+          if (kAhead) fetch(step + kStages, slot, 0, kParts);
+          else if (kKS == 1) fetch(step + kStages - 1, last, 0, 1);
           __builtin_amdgcn_sched_barrier(0);
         }
-        B = Bn;
-      } else {
-        __builtin_amdgcn_sched_barrier(0);
-        if (kAhead) read_first(stage(next));
-        __builtin_amdgcn_sched_barrier(0);
-        if (kAhead) fetch(kb + kStages, slot, 0, kParts);
-        else fetch(kb + kStages - 1, last, 0, 1);
-        __builtin_amdgcn_sched_barrier(0);
       }
-    }
 #pragma unroll
-    for (int rt = 0; rt < 4; ++rt) pend[rt] = p[(kNG - 1) & 1][rt];
-    pend_s = sx[kNG - 1] * cw;
+      for (int rt = 0; rt < 4; ++rt) pend[rt] = p[(kNG - 1) & 1][rt];
+      pend_s = sx[kNG - 1] * cw;
+    }
+    if (kKS > 1) fetch(step + kStages - 1, last, 0, 1);
     slot = next;
   }
 #pragma unroll
   for (int rt = 0; rt < 4; ++rt) acc[rt][kNG - 1] += pend[rt] * pend_s;
   wait_vmcnt<0>();                               // nothing may land in LDS after the workgroup's end
+  if constexpr (kKS > 1) {                       // the waves of the other blocks hand over their sums
+    static_assert(kKS == 2 && kGW * 4 * kNG * 1024 <= kStages * L::kStage, "");
+    v4f* const sums = reinterpret_cast<v4f*>(lds.ring) + w * 4 * kNG * 64 + lane;
+    __syncthreads();
+    if (ks == 1) {
+#pragma unroll
+      for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+        for (int i = 0; i < kNG; ++i) sums[(rt * kNG + i) * 64] = acc[rt][i];
+    }
+    __syncthreads();
+    if (ks == 1) return;
+#pragma unroll
+    for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+      for (int i = 0; i < kNG; ++i) acc[rt][i] += sums[(rt * kNG + i) * 64];
+  }
 
   const int n = n0 + 64 * wm + 16 * lg;
 #pragma unroll
@@ -451,11 +481,11 @@ hipError_t launch_split(const ProductArgs& a, hipStream_t s) {
   return launch<kVariant>(a, s, 64 * kWaves, k_product_split<t.n / 16, t.m / 16, kWaves, kStages, t.most_blocks>);
 }
 
-template <int kVariant, int kNG, int kWN, int kStages>
+template <int kVariant, int kNG, int kWN, int kKS, int kStages>
 hipError_t launch_large(const ProductArgs& a, hipStream_t s) {
-  using L = LargeLds<kNG, kWN, kStages>;
+  using L = LargeLds<kNG, kWN, kKS, kStages>;
   static_assert(L::kBN == kProductTiles[kVariant].n && L::kBM == kProductTiles[kVariant].m, "");
-  return launch<kVariant>(a, s, 512, k_product_large<kNG, kWN, kStages>);
+  return launch<kVariant>(a, s, 512, k_product_large<kNG, kWN, kKS, kStages>);
 }
 
 }  // namespace
@@ -467,11 +497,12 @@ hipError_t launch_product(const ProductArgs& a, hipStream_t s) {
     case 2: return launch_split<2, 4, 3>(a, s);
     case 3: return launch_split<3, 4, 2>(a, s);
     case 4: return launch_split<4, 4, 2>(a, s);
-    case 5: return launch_large<5, 1, 2, 4>(a, s);
-    case 6: return launch_large<6, 2, 2, 4>(a, s);
-    case 7: return launch_large<7, 2, 4, 3>(a, s);
-    case 8: return launch_large<8, 4, 4, 3>(a, s);
-    default: return launch_large<9, 8, 4, 2>(a, s);
+    case 5: return launch_large<5, 1, 2, 1, 4>(a, s);
+    case 6: return launch_large<6, 2, 2, 2, 3>(a, s);
+    case 7: return launch_large<7, 2, 2, 1, 4>(a, s);
+    case 8: return launch_large<8, 2, 4, 1, 3>(a, s);
+    case 9: return launch_large<9, 4, 4, 1, 3>(a, s);
+    default: return launch_large<10, 8, 4, 1, 2>(a, s);
   }
 }
 

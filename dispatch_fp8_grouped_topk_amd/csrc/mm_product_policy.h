@@ -9,10 +9,10 @@ namespace mm {
 // every instance at 72 dense sizes (M 1 to 8192; N, K of 512 x 512, 512 x 7168, 2048 x 2048, 4096 x 7168, 7168 x 2048,
 // 8192 x 512) to within 7 to 16% in the mean: per round of 256 workgroups a fixed part and one for each of the K/128 blocks.
 // The first kProductSplit share K among a workgroup's waves (k_product_split, block time of all its waves together), the
-// others share the tile (k_product_large).  The smallest sum wins; over those sizes and 30 more by 4 to 256 groups the
+// others share the tile (k_product_large; of {128, 64} the second shares K as well).  The smallest sum wins; over those sizes and 30 more by 4 to 256 groups the
 // choice takes 2.7% longer than the best instance in the mean.  Both sides of some borders (us, K 7168, N 4096):
 // M 16 {16, 16} 7.7, {32, 32} 8.5; M 128 {64, 32} 12.5, {64, 64} 17.4; M 256 {64, 64} 18.2, {128, 64} 24.9; M 512 {128, 64}
-// 28.1, {64, 64} 34.4; M 1024 {128, 128} 39.4, {128, 64} 52.3; M 2048 {256, 128} 60.4, {256, 256} 85.4; M 4096 {256, 256} 103,
+// 25.0, {64, 64} 34.4; M 1024 {128, 128} 39.4, {128, 64} 52.3; M 2048 {256, 128} 60.4, {256, 256} 85.4; M 4096 {256, 256} 103,
 // {256, 128} 118.
 struct ProductTile {
   int n, m;
@@ -21,8 +21,8 @@ struct ProductTile {
 };
 constexpr ProductTile kProductTiles[] = {
     {16, 16, 1.9f, .049f, 128}, {16, 32, 1.75f, .073f, 128}, {32, 32, 1.8f, .101f, 128}, {64, 32, 2.3f, .133f, 128},
-    {64, 64, 3.0f, .203f, 112}, {128, 64, 1.75f, .387f, 128}, {128, 128, 2.5f, .498f, 128}, {256, 64, 2.5f, .518f, 128},
-    {256, 128, 3.3f, .724f, 128}, {256, 256, 3.9f, 1.27f, 128}};
+    {64, 64, 3.0f, .203f, 112}, {128, 64, 1.75f, .387f, 128}, {128, 64, 2.4f, .37f, 128}, {128, 128, 2.5f, .498f, 128},
+    {256, 64, 2.5f, .518f, 128}, {256, 128, 3.3f, .724f, 128}, {256, 256, 3.9f, 1.27f, 128}};
 constexpr int kProductCount = sizeof(kProductTiles) / sizeof(kProductTiles[0]), kProductSplit = 5;
 
 // Most workgroups of a launch, whose threads are counted in 32 bits; the largest tile never has more (y alone would pass

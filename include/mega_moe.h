@@ -529,7 +529,7 @@ typedef struct {
  * Block sums are the matrix cores' (see mega_moe_diag_mfma_block_sums), scaled and added up in float32.
  * Rows outside the groups are left as they were in y and not looked at in x.  A row's values depend on its own
  * inputs and its group's weights alone, but the order of their sums, and so their last bits, goes by the problem's
- * sizes and by the row's place in its group.
+ * sizes, by the row's place in its group and by the sizes of the groups before it.
  *   x  u8 (E4M3) [M, K], rows x_stride apart;  x_sf f32 [M, K/128]
  *   w  u8 (E4M3) [G, N, K];  w_sf f32 [G, ceil(N/128), K/128]
  *   group_offset  i32 [G + 1] in device memory (4-byte aligned), ascending (expert_offset of

@@ -377,7 +377,8 @@ DENSE = [(1, 8, 128), (1, 4096, 7168), (2, 24, 256), (5, 520, 1152), (16, 128, 1
          (255, 512, 640), (257, 264, 768), (513, 1016, 1408), (777, 2120, 896), (1500, 384, 256), (2049, 640, 384),
          (4100, 256, 256), (17, 2120, 1152), (1, 4104, 1152), (33, 4104, 1152), (33, 4104, 128), (8200, 24, 1152),
          (8200, 24, 384), (6001, 136, 1152), (8200, 136, 1152), (8200, 136, 128), (50, 40008, 128), (50, 40008, 1152),
-         (8200, 392, 1152), (8200, 392, 128), (2049, 4104, 1152), (8200, 776, 128), (130, 2056, 16384)]
+         (8200, 392, 1152), (8200, 392, 128), (2049, 4104, 1152), (8200, 776, 128), (130, 2056, 16384), (777, 2120, 3712),
+         (300, 4104, 5120), (700, 2120, 5248)]
 
 
 @pytest.mark.parametrize("M,N,K", DENSE)
@@ -398,7 +399,7 @@ def test_dense_product_of_rows_in_wider_buffers(M, N, K, pad):
 GROUPED = [(1, 256, 256, 5, 0), (7, 64, 384, 9, 2), (64, 520, 512, 256, 0), (128, 256, 256, 3, 7), (300, 1032, 640, 17, 33),
            (1024, 512, 1152, 128, 16), (1000, 264, 256, 2, 0), (2000, 384, 512, 8, 100), (4096, 128, 128, 40, 0),
            (3000, 512, 384, 1, 11), (7, 24, 1152, 2, 0), (300, 24, 128, 128, 0), (7, 2120, 384, 3, 0), (1000, 264, 1152, 40, 9),
-           (2000, 520, 128, 40, 0), (2000, 1032, 384, 40, 9), (4096, 1032, 128, 40, 5), (3000, 520, 1152, 20, 0)]
+           (2000, 520, 128, 40, 0), (2000, 1032, 384, 40, 9), (4096, 1032, 128, 40, 5), (3000, 520, 1152, 20, 0), (300, 1032, 3712, 17, 0), (600, 2120, 3712, 3, 9), (600, 2120, 5120, 3, 9)]
 
 
 @pytest.mark.parametrize("M,N,K,G,behind", GROUPED)

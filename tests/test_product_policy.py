@@ -41,8 +41,10 @@ def test_gpu_shapes_reach_every_kernel_and_tile(lib):
         n, m = lib.pp_n(v), lib.pp_m(v)
         assert any(M % m and N % n for M, N, _ in shapes), (n, m)          # ragged both ways
         assert any(K // 128 % 4 for _, _, K in shapes), (n, m)             # scales of a part of four blocks
-        assert v < 5 or any(K <= 256 for _, _, K in shapes), (n, m)        # fewer blocks than a ring holds
+        # fewer blocks than a ring holds; the second {128, 64} shares K, for long ones only
+        assert v < 5 or v == 6 or any(K <= 256 for _, _, K in shapes), (n, m)
         assert any(K >= 1024 for _, _, K in shapes), (n, m)                # and more
+    assert {K // 128 % 2 for _, _, K in dense[6]} == {0, 1}                # both sets of waves have a last block, or one
     grouped = {lib.pp_variant(M, N, K, G) for M, N, K, G, _ in gpu.GROUPED if G > 1}
     assert grouped == every, every - grouped
 
