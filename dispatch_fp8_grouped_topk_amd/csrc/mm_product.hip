@@ -38,7 +38,7 @@ __device__ __forceinline__ void group_rows(const ProductArgs& a, int g, int& lo,
 // ring in LDS by loads that need no registers; a block's MFMAs run while the next ones are on their way.  16-byte chunk c of
 // a row r sits at c ^ (r / 2 % 8), so that the 16 rows of an operand read fall into different banks.
 //
-// 8192 x 4096 x 7168 in tiles of 256 x 256 takes 217 us, 2215 TFLOP/s, of the 159 us at the 3025 TFLOP/s that a large library
+// 8192 x 4096 x 7168 in tiles of 256 x 256 takes 217 to 231 us by box, 2080 to 2215 TFLOP/s, of the 159 us at the 3025 TFLOP/s that a large library
 // product with one scale a tensor reaches here.  The matrix units are busy 47% of the cycles at the 2.1 GHz of the loaded chip;
 // a block takes about 4000 cycles for 2048 of MFMAs: the scaling (four multiply-adds an MFMA) runs beside the MFMAs in a
 // register-only loop (4% longer than without), LDS is busy a quarter of the time, and with every workgroup on the same tile,

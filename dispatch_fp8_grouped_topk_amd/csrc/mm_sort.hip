@@ -189,8 +189,8 @@ __global__ __launch_bounds__(1024) void k_sort_bases(SortArgs a) {
 
 // 3. Places and rows: a wave takes a token, reads its row once and writes it k times, past the caches.  Every workgroup makes
 // the experts' offsets from their totals itself (a kilobyte at 256 experts) rather than in a launch of their own.
-// T 8192, H 7168, E 256, k 8 in BF16 (1.02 GB, a floor of 201 us at the rate of a large copy) takes 205 us, and 10 us for the two
-// kernels before: bound by writing.  Stores through the caches took 328; the other way round, a wave a place that reads its
+// T 8192, H 7168, E 256, k 8 in BF16 (1.02 GB, a floor of 201 us at the rate of a large copy) takes 216 us with the two
+// kernels before (10): bound by writing.  Stores through the caches took 328; the other way round, a wave a place that reads its
 // token's row from the caches, 257 with stores past them and 310 to 575 through them.
 template <bool kMove>
 __global__ __launch_bounds__(256) void k_sort_move(SortArgs a) {
