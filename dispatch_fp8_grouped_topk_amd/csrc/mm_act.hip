@@ -140,7 +140,8 @@ __global__ __launch_bounds__(256) void k_act_backward(ActArgs a) {
     rd.values(d);
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
-      const bool keep_g = !inputs || !(fabsf(g[n]) > a.clamp), keep_u = !inputs || !(fabsf(u[n]) > a.clamp);
+      // what the clamp drops is selected, not multiplied by 0: the other factors may not be finite
+      bool keep_g = !inputs || !(fabsf(g[n]) > a.clamp), keep_u = !inputs || !(fabsf(u[n]) > a.clamp);
       if (inputs) {
         g[n] = clamped(g[n], a.clamp);
         u[n] = clamped(u[n], a.clamp);
@@ -151,7 +152,7 @@ __global__ __launch_bounds__(256) void k_act_backward(ActArgs a) {
         const float v = fabsf(silu * u[n]);
         bool outside = v > a.clamp;
         if (fabsf(v - a.clamp) <= kClose * a.clamp) outside = fabs(swiglu64(g[n], u[n], 0.f, false)) > (double)a.clamp;
-        if (outside) d[n] = 0.f;
+        if (outside) keep_g = keep_u = false;
       }
       const float du = d[n] * silu;
       g[n] = keep_g ? d[n] * u[n] * s.s * (1.0f + g[n] * s.rest) : 0.f;

@@ -101,10 +101,10 @@ def act_backward(x, d, clamp=0.0, inputs=False):
     with np.errstate(over="ignore"):
         s = 1.0 / (1.0 + np.exp(-g))
         rest = 1.0 / (1.0 + np.exp(g))
-    if clamp and not inputs:
-        d = np.where(np.abs(g * s * u) > clamp, 0.0, d)
     d_g, d_u = d * u * s * (1 + g * rest), d * g * s
     mag = np.abs(d * u * s) * (1 + np.abs(g * rest))
+    if clamp and not inputs:                           # selected: the dropped terms may not be finite
+        d_g, d_u, mag = (np.where(np.abs(g * s * u) > clamp, 0.0, v) for v in (d_g, d_u, mag))
     if clamp and inputs:
         d_g, mag = (np.where(np.abs(g0) > clamp, 0.0, v) for v in (d_g, mag))
         d_u = np.where(np.abs(u0) > clamp, 0.0, d_u)

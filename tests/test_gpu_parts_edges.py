@@ -1,0 +1,72 @@
+"""Values of the layer in parts that few batches hold, on an MI355X: gradients where the clamp drops a value that is not
+finite.
+"""
+import numpy as np
+import pytest
+import torch
+
+import dispatch_fp8_grouped_topk_amd as mm
+from oracle import parts
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": (mm.DTYPE_BF16, torch.bfloat16), "f32": (mm.DTYPE_F32, torch.float32)}
+INF = float("inf")
+
+
+def _say(*a):
+    print("[edges]", *a, flush=True)
+
+
+def _f64(t):
+    return t.double().cpu().numpy()
+
+
+def _backward(x, d, clamp=0.0, inputs=False):
+    kind = mm.DTYPE_BF16 if x.dtype == torch.bfloat16 else mm.DTYPE_F32
+    d_x = torch.full_like(x, 7.0)
+    p = mm.ActProblem.make(x.shape[0], x.shape[1] // 2, x_dtype=kind, swiglu_clamp=clamp,
+                           flags=mm.FLAG_CLAMP_INPUTS if inputs else 0)
+    mm.mega_moe_act_backward(p, x, d, d_x)
+    return d_x
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_gradients_of_what_the_clamp_drops_are_zero(kind):
+    """silu(g) u outside [-c, c]: both gradients are 0, whatever g, u and d are; a neighbour's are what they were."""
+    _say("dropped", kind)
+    I, c = 128, 2.0
+    pairs = [(INF, 1.0), (INF, -1.0), (1.0, INF), (3.0, -INF), (-1.0, INF), (INF, INF), (INF, -INF), (1e3, 1e38), (5.0, 5.0)]
+    g = torch.Generator().manual_seed(1)
+    x = (torch.randn(2, 2 * I, generator=g) * 0.5).to(DT[kind][1]).cuda()
+    d = torch.randn(2, I, generator=g).to(DT[kind][1]).cuda()
+    ref = _backward(x, d, c)
+    for i, (gate, up) in enumerate(pairs):
+        x[0, 3 * i], x[0, I + 3 * i] = gate, up
+    x[1, 7], x[1, I + 7], d[1, 7] = 9.0, 9.0, INF
+    got = _backward(x, d, c)
+    at = [3 * i for i in range(len(pairs))]
+    assert (got[0, at] == 0).all() and (got[0, [I + i for i in at]] == 0).all()
+    assert got[1, 7] == 0 and got[1, I + 7] == 0
+    same = torch.ones_like(got, dtype=torch.bool)
+    same[0, at], same[0, [I + i for i in at]], same[1, [7, I + 7]] = False, False, False
+    assert torch.equal(got[same], ref[same])
+    with np.errstate(invalid="ignore"):
+        want, _ = parts.act_backward(_f64(x), _f64(d), c)
+    assert (want[0, at] == 0).all() and np.isfinite(want).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_gradients_of_clamped_inputs_that_are_not_finite(kind):
+    """Each input outside its clamp has the gradient 0, the other one the clamped input's."""
+    _say("inputs", kind)
+    I, c = 128, 2.0
+    x = torch.ones(1, 2 * I, dtype=DT[kind][1], device="cuda")
+    d = torch.ones(1, I, dtype=DT[kind][1], device="cuda")
+    for i, (gate, up) in enumerate([(INF, 1.0), (-INF, 1.0), (1.0, INF), (1.0, -INF), (INF, -INF)]):
+        x[0, i], x[0, I + i] = gate, up
+    got = _backward(x, d, c, True)
+    capped = x.clamp(-c, c)
+    ref = _backward(capped, d)                                      # within the clamp there is none
+    outside = x.abs() > c
+    assert (got[outside] == 0).all() and torch.equal(got[~outside], ref[~outside])
