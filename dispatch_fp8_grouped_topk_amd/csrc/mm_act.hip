@@ -5,27 +5,71 @@
 //   d_u = d g s,  d_g = d u s (1 + g (1 - s))
 //
 // One pass, eight columns a lane, nothing shared beyond 16 lanes, so the grid is flat over all pieces of all rows.  Bound by
-// memory: 65536 x 2048 from BF16 with float scales (665 MB) takes 124 us, 5.3 TB/s; the gradient of 4093 x 1536 in float32
-// (126 MB) 21.3 us, 5.9 TB/s, its stores past the caches (through them 25.3; the 8-bit rows, read next, gain nothing).
+// memory: 65536 x 2048 from BF16 with float scales (665 MB) takes 123 us, 5.4 TB/s; the gradient of 4093 x 1536 in float32
+// (126 MB) 21.1 us, 6.0 TB/s, its stores past the caches (through them 25.3; the 8-bit rows, read next, gain nothing).
 //
 // Numerics: float32 throughout.  With e = exp(-|g|) in (0, 1] and r = 1 / (1 + e), s and 1 - s are r and e r or the other
-// way round: neither overflows or cancels.  The hardware's exponential takes g log2(e), rounded: its relative error is
-// at most 2^-17 (|g| 88; beyond, e is below float32's normal numbers) and 2^-21 for |g| up to 6.  Where that decides something that
-// jumps, a UE8M0 code or whether a value lies inside the clamp, it is decided again in float64.
+// way round: neither overflows or cancels.  |g| log2(e) is taken in two parts, the product and what its rounding left: in one
+// part it would cost |g| half steps of e.  v is within 9 half steps of float32 then (2^-24 of the value each).  Beyond
+// |g| 86, where e may be no normal number, it is kept as f 2^n and the power applied to the other factor.  Where an error
+// decides something that jumps, a UE8M0 code or whether a value lies inside the clamp, it is decided again in float64.
+#include <type_traits>
+
 #include "mm_parts.h"
 #include "mm_rows.h"
 
 namespace mm {
 namespace {
 
-constexpr float kClose = 1.0f / 65536;           // twice the largest relative error of v
+constexpr float kClose = 1.0f / 65536;           // far more than the largest relative error of v
+constexpr float kFarGate = 86.f;                 // exp(-86) is still a normal number
 
+// e = exp(-|g|) = f 2^n (n 0 unless kFar) and r = 1 / (1 + e).  A NaN stays one in what g is multiplied with.
 struct Sigmoid {
-  float s, rest;                                 // s(g) and 1 - s(g)
+  float r, e, f;
+  int n;
 };
+template <bool kFar>
 __device__ __forceinline__ Sigmoid sigmoid(float g) {
-  const float e = __expf(-fabsf(g)), r = __builtin_amdgcn_rcpf(1.0f + e);
-  return g >= 0.f ? Sigmoid{r, e * r} : Sigmoid{e * r, r};
+  constexpr float kHi = 1.44269502f, kLo = 1.92596299e-8f;      // log2(e)
+  const float a = kFar ? fminf(fabsf(g), 400.f) : fabsf(g);     // 2^-577 is 0 times any float
+  const float t = a * kHi;
+  Sigmoid s;
+  if constexpr (kFar) {
+    const float whole = __builtin_rintf(t);
+    s.f = __builtin_amdgcn_exp2f(__builtin_fmaf(-a, kLo, __builtin_fmaf(-a, kHi, whole)));
+    s.n = -(int)whole;
+    s.e = __builtin_ldexpf(s.f, s.n);
+  } else {
+    const float p = __builtin_amdgcn_exp2f(-t), rest = __builtin_fmaf(a, kLo, __builtin_fmaf(a, kHi, -t));
+    s.e = s.f = __builtin_fmaf(p, rest * -0.693147181f, p);      // 2^-rest to first order: rest is below 2^-17
+    s.n = 0;
+  }
+  const float d = 1.0f + s.e, r = __builtin_amdgcn_rcpf(d);
+  s.r = __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
+  return s;
+}
+
+// x s(g)
+template <bool kFar>
+__device__ __forceinline__ float times_sigmoid(float x, float g, const Sigmoid& s) {
+  if constexpr (kFar) return (g < 0.f ? __builtin_ldexpf(x, s.n) * s.f : x) * s.r;
+  return x * (g < 0.f ? s.e * s.r : s.r);
+}
+// x silu(g)
+template <bool kFar>
+__device__ __forceinline__ float times_silu(float x, float g, const Sigmoid& s) {
+  if constexpr (kFar) return (g < 0.f ? __builtin_ldexpf(x, s.n) * s.f : x) * (g * s.r);
+  return g * (g < 0.f ? s.e * s.r : s.r) * x;
+}
+
+// Gates far out are taken again by themselves, so that a value depends on its own inputs alone.
+__device__ __forceinline__ bool far_out(float g) { return fabsf(g) > kFarGate; }
+__device__ __forceinline__ bool any_far(const float (&g)[8]) {
+  float m = 0.f;
+#pragma unroll
+  for (int n = 0; n < 8; ++n) m = fmaxf(m, fabsf(g[n]));
+  return far_out(m);
 }
 
 // v in [-c, c]; NaN stays NaN.
@@ -34,10 +78,29 @@ __device__ __forceinline__ T clamped(T v, T c) {
   return v > c ? c : v < -c ? -c : v;
 }
 
+__device__ __forceinline__ void clamp_all(float (&v)[8], float c) {
+#pragma unroll
+  for (int n = 0; n < 8; ++n) v[n] = clamped(v[n], c);
+}
+
 __device__ __forceinline__ double swiglu64(float g, float u, float c, bool inputs) {
   const double gd = inputs ? clamped(g, c) : g, ud = inputs ? clamped(u, c) : u;
   const double v = gd / (1.0 + exp(-gd)) * ud;
   return c > 0.f && !inputs ? clamped(v, (double)c) : v;
+}
+
+// Piece 256 b + threadIdx.x of eight columns among those of all rows: its row and its place there, without a division in
+// 64 bits (about a hundred instructions a thread: 65536 x 2048 150 -> 145 us where arithmetic was the bound).  A row has 16 j pieces, so b starts in row 16 b / j: the high half of
+// 16 b ceil(2^64 / j), exact as 16 b j < 2^64; from there less than 2304 pieces are counted, the high part of a product with
+// ceil(2^24 / 16 j), exact as 2304 * 2048 < 2^24.
+struct Piece {
+  int64_t row;
+  int c;
+};
+__device__ __forceinline__ Piece piece(const ActArgs& a, uint64_t b, int cpt) {
+  const uint64_t row = a.by_row ? __umul64hi(16 * b, a.by_row) : 16 * b;
+  const uint32_t c = (uint32_t)(256 * b - row * (uint32_t)cpt) + threadIdx.x, more = c * a.by_piece >> 24;
+  return {(int64_t)(row + more), (int)(c - more * (uint32_t)cpt)};
 }
 
 // Rows that are looked at.
@@ -50,9 +113,8 @@ __global__ __launch_bounds__(256) void k_act_quant(ActArgs a) {
   const int cpt = a.I / 8;
   const int64_t total = (int64_t)rows_used(a) * cpt;
   const bool inputs = a.clamp > 0.f && a.clamp_inputs, output = a.clamp > 0.f && !a.clamp_inputs;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t row = i / cpt;
-    const int c = (int)(i - row * cpt);
+  for (uint64_t b = blockIdx.x; (int64_t)(256 * b + threadIdx.x) < total; b += gridDim.x) {
+    const auto [row, c] = piece(a, b, cpt);
     Raw<kF32> raw, raw_u;
     raw.load(a.x, (size_t)row * a.x_stride + 8 * c);
     if constexpr (kSwiglu) raw_u.load(a.x, (size_t)row * a.x_stride + a.I + 8 * c);
@@ -60,16 +122,15 @@ __global__ __launch_bounds__(256) void k_act_quant(ActArgs a) {
     raw.values(g);
     if constexpr (kSwiglu) {
       raw_u.values(u);
+      if (inputs) clamp_all(g, a.clamp), clamp_all(u, a.clamp);
 #pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        float gn = g[n], un = u[n];
-        if (inputs) {
-          gn = clamped(gn, a.clamp);
-          un = clamped(un, a.clamp);
-        }
-        v[n] = gn * sigmoid(gn).s * un;
-        if (output) v[n] = clamped(v[n], a.clamp);
+      for (int n = 0; n < 8; ++n) v[n] = times_silu<false>(u[n], g[n], sigmoid<false>(g[n]));
+      if (any_far(g)) {
+#pragma unroll
+        for (int n = 0; n < 8; ++n)
+          if (far_out(g[n])) v[n] = times_silu<true>(u[n], g[n], sigmoid<true>(g[n]));
       }
+      if (output) clamp_all(v, a.clamp);
     } else {
 #pragma unroll
       for (int n = 0; n < 8; ++n) v[n] = g[n];
@@ -121,14 +182,14 @@ __global__ __launch_bounds__(256) void k_act_quant(ActArgs a) {
   }
 }
 
-template <bool kF32>
+// kClamp: none, of the inputs, of the output; an instance of its own keeps the float64 decision's registers out of the others.
+enum Clamp { kClampNone, kClampInputs, kClampOutput };
+template <bool kF32, Clamp kClamp>
 __global__ __launch_bounds__(256) void k_act_backward(ActArgs a) {
   const int cpt = a.I / 8;
   const int64_t total = (int64_t)rows_used(a) * cpt;
-  const bool inputs = a.clamp > 0.f && a.clamp_inputs, output = a.clamp > 0.f && !a.clamp_inputs;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t row = i / cpt;
-    const int c = (int)(i - row * cpt);
+  for (uint64_t b = blockIdx.x; (int64_t)(256 * b + threadIdx.x) < total; b += gridDim.x) {
+    const auto [row, c] = piece(a, b, cpt);
     const size_t at = (size_t)row * a.x_stride + 8 * c;
     Raw<kF32> rg, ru, rd;
     rg.load(a.x, at);
@@ -138,29 +199,57 @@ __global__ __launch_bounds__(256) void k_act_backward(ActArgs a) {
     rg.values(g);
     ru.values(u);
     rd.values(d);
+    // what the clamp drops is selected, not multiplied by 0: the other factors may not be finite
+    uint32_t drop_g = 0, drop_u = 0;
+    if constexpr (kClamp == kClampInputs) {
 #pragma unroll
-    for (int n = 0; n < 8; ++n) {
-      // what the clamp drops is selected, not multiplied by 0: the other factors may not be finite
-      bool keep_g = !inputs || !(fabsf(g[n]) > a.clamp), keep_u = !inputs || !(fabsf(u[n]) > a.clamp);
-      if (inputs) {
-        g[n] = clamped(g[n], a.clamp);
-        u[n] = clamped(u[n], a.clamp);
+      for (int n = 0; n < 8; ++n) {
+        drop_g |= (uint32_t)(fabsf(g[n]) > a.clamp) << n;
+        drop_u |= (uint32_t)(fabsf(u[n]) > a.clamp) << n;
       }
-      const Sigmoid s = sigmoid(g[n]);
-      const float silu = g[n] * s.s;
-      if (output) {
-        const float v = fabsf(silu * u[n]);
-        bool outside = v > a.clamp;
-        if (fabsf(v - a.clamp) <= kClose * a.clamp) outside = fabs(swiglu64(g[n], u[n], 0.f, false)) > (double)a.clamp;
-        if (outside) keep_g = keep_u = false;
-      }
-      const float du = d[n] * silu;
-      g[n] = keep_g ? d[n] * u[n] * s.s * (1.0f + g[n] * s.rest) : 0.f;
-      u[n] = keep_u ? du : 0.f;
+      clamp_all(g, a.clamp), clamp_all(u, a.clamp);
     }
-    store8_nt<kF32>(a.d_x, at, g);
-    store8_nt<kF32>(a.d_x, at + a.I, u);
+    float d_g[8], d_u[8], v[8];
+    const auto gradient = [&](int n, auto far) {
+      constexpr bool kFar = decltype(far)::value;
+      const Sigmoid s = sigmoid<kFar>(g[n]);
+      const float rest = g[n] < 0.f ? s.r : s.e * s.r;
+      d_g[n] = times_sigmoid<kFar>(d[n] * u[n], g[n], s) * __builtin_fmaf(g[n], rest, 1.0f);
+      d_u[n] = times_silu<kFar>(d[n], g[n], s);
+      if constexpr (kClamp == kClampOutput) v[n] = fabsf(times_silu<kFar>(u[n], g[n], s));
+    };
+#pragma unroll
+    for (int n = 0; n < 8; ++n) gradient(n, std::false_type{});
+    if (any_far(g)) {
+#pragma unroll
+      for (int n = 0; n < 8; ++n)
+        if (far_out(g[n])) gradient(n, std::true_type{});
+    }
+    if constexpr (kClamp == kClampOutput) {
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        bool outside = v[n] > a.clamp;
+        if (fabsf(v[n] - a.clamp) <= kClose * a.clamp) outside = fabs(swiglu64(g[n], u[n], 0.f, false)) > (double)a.clamp;
+        drop_g |= (uint32_t)outside << n;
+      }
+      drop_u = drop_g;
+    }
+    if constexpr (kClamp != kClampNone) {
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        d_g[n] = drop_g >> n & 1 ? 0.f : d_g[n];
+        d_u[n] = drop_u >> n & 1 ? 0.f : d_u[n];
+      }
+    }
+    store8_nt<kF32>(a.d_x, at, d_g);
+    store8_nt<kF32>(a.d_x, at + a.I, d_u);
   }
+}
+
+ActArgs with_pieces(ActArgs a) {
+  a.by_row = a.I == 128 ? 0 : ~0ull / (unsigned)(a.I / 128) + 1;       // 2^64 itself does not fit
+  a.by_piece = ((1u << 24) + a.I / 8 - 1) / (a.I / 8);
+  return a;
 }
 
 unsigned pieces_grid(const ActArgs& a) {
@@ -169,8 +258,16 @@ unsigned pieces_grid(const ActArgs& a) {
 
 template <bool kF32, bool kSwiglu>
 void launch_quant(const ActArgs& a, hipStream_t s) {
-  if (a.per32) hipLaunchKernelGGL((k_act_quant<kF32, kSwiglu, true>), dim3(pieces_grid(a)), dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((k_act_quant<kF32, kSwiglu, false>), dim3(pieces_grid(a)), dim3(256), 0, s, a);
+  if (a.per32) hipLaunchKernelGGL((k_act_quant<kF32, kSwiglu, true>), dim3(pieces_grid(a)), dim3(256), 0, s, with_pieces(a));
+  else hipLaunchKernelGGL((k_act_quant<kF32, kSwiglu, false>), dim3(pieces_grid(a)), dim3(256), 0, s, with_pieces(a));
+}
+
+template <bool kF32>
+void launch_backward(const ActArgs& a, hipStream_t s) {
+  const dim3 grid(pieces_grid(a)), threads(256);
+  if (!(a.clamp > 0.f)) hipLaunchKernelGGL((k_act_backward<kF32, kClampNone>), grid, threads, 0, s, with_pieces(a));
+  else if (a.clamp_inputs) hipLaunchKernelGGL((k_act_backward<kF32, kClampInputs>), grid, threads, 0, s, with_pieces(a));
+  else hipLaunchKernelGGL((k_act_backward<kF32, kClampOutput>), grid, threads, 0, s, with_pieces(a));
 }
 
 }  // namespace
@@ -182,8 +279,7 @@ hipError_t launch_act_quant(const ActArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_act_backward(const ActArgs& a, hipStream_t s) {
-  if (a.f32) hipLaunchKernelGGL(k_act_backward<true>, dim3(pieces_grid(a)), dim3(256), 0, s, a);
-  else hipLaunchKernelGGL(k_act_backward<false>, dim3(pieces_grid(a)), dim3(256), 0, s, a);
+  a.f32 ? launch_backward<true>(a, s) : launch_backward<false>(a, s);
   return hipGetLastError();
 }
 

@@ -80,6 +80,8 @@ struct ActArgs {
   float clamp;               // <= 0: none
   int clamp_inputs;
   int swiglu, f32, per32;
+  uint64_t by_row;           // factors that take the place of divisions (csrc/mm_act.hip sets them)
+  uint32_t by_piece;
 };
 
 hipError_t launch_act_quant(const ActArgs& a, hipStream_t s);

@@ -561,9 +561,9 @@ typedef struct {
  *   v = clamp(silu(g) * u)         (MEGA_MOE_ACT_SWIGLU, x [M, 2I]: g the first I columns, u the others; with
  *                                   MEGA_MOE_FLAG_CLAMP_INPUTS the clamp is on g and u instead)
  *   q, q_sf = v in 8 bits with the recipe's scales, out = bf16(v)
- * in float32 (silu with the hardware's exponential and reciprocal, a few ulp; it may be 0 for g below -87.3, where the
- * exponential is no normal number), each output rounded once; scales and codes as mega_moe_norm_quant makes them, a UE8M0 code decided as if in float64.  A group with a v that is
- * not finite has NaN q and q_sf; others are not affected.
+ * in float32 (v within 9 half steps, 2^-24 of its value each, or within 2^-141), each output rounded once; scales and codes
+ * as mega_moe_norm_quant makes them, a UE8M0 code decided as if in float64.  A group with a v that is not finite has NaN q
+ * and q_sf; others are not affected.
  *   x          [M, I] | [M, 2I] x_dtype, rows x_stride apart
  *   num_valid  i32 [1] in device memory (4-byte aligned) or NULL: rows from *num_valid on are not looked at, and
  *              left as they were in the outputs (expert_offset + E of mega_moe_sort_tokens, say)
@@ -576,7 +576,8 @@ int mega_moe_act_quant(const mega_moe_act_problem* p, const void* x, const int32
  * 8 bits passes gradients on as they are), with s = 1 / (1 + exp(-g)):
  *   d_g = d_out * u * s * (1 + g (1 - s)),  d_u = d_out * g * s
  * both 0 where silu(g) * u lies outside [-c, c] (decided as in float64), or with MEGA_MOE_FLAG_CLAMP_INPUTS each
- * where its own input does (g and u in the formulas are then the clamped ones); in float32, rounded once.
+ * where its own input does (g and u in the formulas are then the clamped ones); in float32 (d_u within 9 half steps, d_g
+ * within 18 of |d_out u s| (1 + |g (1 - s)|), or both within 2^-141), rounded once.
  *   x [M, 2I] x_dtype, rows x_stride apart;  d_out [M, I] x_dtype;  num_valid as above
  *   d_x [M, 2I] x_dtype, rows x_stride apart; may be x itself */
 int mega_moe_act_backward(const mega_moe_act_problem* p, const void* x, const void* d_out, const int32_t* num_valid,

@@ -1,5 +1,5 @@
 """Values of the layer in parts that few batches hold, on an MI355X: gradients where the clamp drops a value that is not
-finite.
+finite, and rows of every width.
 """
 import numpy as np
 import pytest
@@ -70,3 +70,21 @@ def test_gradients_of_clamped_inputs_that_are_not_finite(kind):
     ref = _backward(capped, d)                                      # within the clamp there is none
     outside = x.abs() > c
     assert (got[outside] == 0).all() and torch.equal(got[~outside], ref[~outside])
+
+
+def _copied(M, I):
+    x = torch.randn(M, I, device="cuda").to(torch.bfloat16)
+    out = torch.zeros_like(x)
+    mm.mega_moe_act_quant(mm.ActProblem.make(M, I, mm.ACT_NONE), x, out=out)
+    return torch.equal(out.view(torch.int16), x.view(torch.int16))
+
+
+def test_every_width_finds_its_rows():
+    """Without an activation the BF16 output is the input: each piece of eight columns has to find its row and place."""
+    assert [j for j in range(1, 129) if not _copied(67, 128 * j)] == []
+
+
+@pytest.mark.parametrize("M,I", [(3000001, 128), (1400003, 384), (70001, 128 * 127), (524309, 128 * 13)])
+def test_many_rows_of_a_width_find_theirs(M, I):
+    _say("rows", M, I)
+    assert _copied(M, I)
