@@ -21,7 +21,9 @@
 namespace mm {
 namespace {
 
-constexpr float kClose = 1.0f / 65536;           // far more than the largest relative error of v
+// Float64 decides within kClose of a border, thirty times v's error, and kSmall, twice what v may be off by where float32 has
+// few bits left.
+constexpr float kClose = 1.0f / 65536, kSmall = 0x1p-140f;
 constexpr float kFarGate = 86.f;                 // exp(-86) is still a normal number
 
 // e = exp(-|g|) = f 2^n (n 0 unless kFar) and r = 1 / (1 + e).  A NaN stays one in what g is multiplied with.
@@ -157,8 +159,9 @@ __global__ __launch_bounds__(256) void k_act_quant(ActArgs a) {
       const float r = __uint_as_float(m) * (1.0f / 448.0f);
       const uint32_t b = __float_as_uint(r), man = b & 0x7FFFFFu;
       uint32_t code = min((b >> 23) + 1, 254u);
-      // kClose of the mantissa on either side of a power of two; the same in the four lanes of a group
-      if (man <= 128 || man >= 0x7FFFFFu - 128 || b < 0x00800000u) {
+      // kClose on either side of a power of two: 128 steps above it, 256 of half the size below; below float32's normal numbers
+      // always.  The same in the four lanes of a group.
+      if (man <= 128 || man >= 0x800000u - 256 || b < 0x00800000u) {
         double d = 0.0;
 #pragma unroll
         for (int n = 0; n < 8; ++n) d = fmax(d, fabs(kSwiglu ? swiglu64(g[n], u[n], a.clamp, inputs) : (double)g[n]));
@@ -226,10 +229,13 @@ __global__ __launch_bounds__(256) void k_act_backward(ActArgs a) {
         if (far_out(g[n])) gradient(n, std::true_type{});
     }
     if constexpr (kClamp == kClampOutput) {
+      // near the largest numbers near_hi is infinite, and so may v be
+      const float near_lo = __builtin_fmaf(a.clamp, -kClose, a.clamp) - kSmall;
+      const float near_hi = __builtin_fmaf(a.clamp, kClose, a.clamp) + kSmall;
 #pragma unroll
       for (int n = 0; n < 8; ++n) {
         bool outside = v[n] > a.clamp;
-        if (fabsf(v[n] - a.clamp) <= kClose * a.clamp) outside = fabs(swiglu64(g[n], u[n], 0.f, false)) > (double)a.clamp;
+        if (v[n] >= near_lo && !(v[n] > near_hi)) outside = fabs(swiglu64(g[n], u[n], 0.f, false)) > (double)a.clamp;
         drop_g |= (uint32_t)outside << n;
       }
       drop_u = drop_g;

@@ -88,3 +88,31 @@ def test_every_width_finds_its_rows():
 def test_many_rows_of_a_width_find_theirs(M, I):
     _say("rows", M, I)
     assert _copied(M, I)
+
+
+@pytest.mark.parametrize("clamp", [3.4028234663852886e38, 2.0 ** -120, 2.0 ** -126, 2.0 ** -134])
+def test_gradients_next_to_clamps_at_either_end_of_float32(clamp):
+    """silu(g) u within float32 steps of a clamp near the largest and the smallest numbers, where the float32 product
+    overflows or has few bits left: kept or dropped as the float64 value says."""
+    _say("clamp", clamp)
+    M, I = 32, 1024
+    rng = np.random.default_rng(5)
+    g = np.where(rng.random((M, I)) < 0.5, rng.uniform(0.2, 6, (M, I)), rng.uniform(-12, -3, (M, I))).astype(np.float32)
+    g64 = g.astype(np.float64)
+    if clamp < 1:
+        g = np.where(rng.random((M, I)) < 0.5, g, rng.uniform(-100, -87, (M, I)).astype(np.float32))
+        g64 = g.astype(np.float64)
+    else:
+        g = np.abs(g) + np.float32(2)                                # silu(g) above 1: `up` is a float32 number
+        g64 = g.astype(np.float64)
+    silu = g64 / (1 + np.exp(-g64))
+    u = (clamp / silu).astype(np.float32)
+    for _ in range(3):
+        u = np.where(rng.random((M, I)) < 0.5, np.nextafter(u, np.copysign(np.float32(np.inf), u)), np.nextafter(u, np.float32(0)))
+    assert np.isfinite(u).all()
+    x = torch.from_numpy(np.concatenate([g, u], axis=1)).cuda()
+    d = torch.full((M, I), 1e8 if clamp < 1 else 1e-8, device="cuda")
+    got = _f64(_backward(x, d, clamp))
+    outside = np.abs(silu * u.astype(np.float64)) > clamp
+    assert outside.any() and not outside.all()
+    assert np.array_equal(got[:, I:] == 0, outside)
