@@ -551,13 +551,14 @@ _binding_module = None
 
 
 def _compiled():
-    """The compiled part of the binding (argument checks of the operators in front of the layer)."""
+    """The compiled part of the binding (argument checks of the operators in front of the layer and the layer in parts)."""
     global _binding_module
     if _binding_module is None:
         _load()                              # torch and the library it links to
         if not os.path.exists(os.path.join(HERE, "_binding.so")):
             raise ImportError("_binding.so is missing; build it with `python -m dispatch_fp8_grouped_topk_amd.build`")
         from . import _binding as module
+        module.problem_classes(NormProblem, GateProblem, TopkProblem, SortProblem, UnsortProblem, ProductProblem, ActProblem)
         _binding_module = module
     return _binding_module
 

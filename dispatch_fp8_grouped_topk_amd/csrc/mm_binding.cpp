@@ -3,6 +3,8 @@
 // checks torch tensors against the problem, takes the stream and calls the C ABI (mega_moe.h); the
 // status goes back to Python.  No arithmetic happens here.
 //
+// problem_classes(NormProblem, GateProblem, TopkProblem, SortProblem, UnsortProblem, ProductProblem, ActProblem): once, before
+// the first call
 // norm_quant(problem, x, weight, residual, residual_out, normed, q, q_sf, stream) -> status
 // gate_logits(problem, x, weight, logits, stream) -> status
 // gate_topk(problem, logits, topk_idx, topk_w, bias, num_valid, stream) -> status
@@ -13,7 +15,7 @@
 // act_quant(problem, x, num_valid, q, q_sf, out, stream) -> status
 // act_backward(problem, x, d_out, num_valid, d_x, stream) -> status
 //
-// problem: a ctypes structure; stream: an int handle, or None for the current stream of the
+// problem: an instance of its operator's class; stream: an int handle, or None for the current stream of the
 // tensors' device, which is made the current device for the call.
 #include <Python.h>
 
@@ -78,20 +80,53 @@ at::Device device_of(const at::Tensor& t, const char* what) {
 
 void* ptr(const at::Tensor* t) { return t && t->numel() ? t->data_ptr() : nullptr; }
 
-// The problem structure behind a ctypes instance, copied.
+// The ctypes classes of the problem structures, as the package hands them over: structures of different operators have the
+// same size, so only the class tells them apart.
+template <class P>
+PyObject* g_problem_class = nullptr;
+
+// The problem structure behind an instance of its class, copied.
 template <class P>
 P problem_of(PyObject* o) {
+  PyObject* const cls = g_problem_class<P>;
+  const int is = cls ? PyObject_IsInstance(o, cls) : 0;
   Py_buffer b;
-  if (PyObject_GetBuffer(o, &b, PyBUF_SIMPLE)) {
+  if (is <= 0 || PyObject_GetBuffer(o, &b, PyBUF_SIMPLE)) {
     PyErr_Clear();
     throw Refused("problem must be the operator's problem structure");
   }
-  const bool fits = b.len == (Py_ssize_t)sizeof(P);
+  const bool fits = b.len >= (Py_ssize_t)sizeof(P);      // a subclass may have fields of its own
   P p{};
   if (fits) std::memcpy(&p, b.buf, sizeof(P));
   PyBuffer_Release(&b);
   if (!fits) throw Refused("problem must be the operator's problem structure");
   return p;
+}
+
+template <class P>
+void take_class(PyObject* cls) {
+  Py_INCREF(cls);
+  Py_XSETREF(g_problem_class<P>, cls);
+}
+
+PyObject* problem_classes(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  if (n != 7) {
+    PyErr_SetString(PyExc_TypeError, "problem_classes takes 7 classes");
+    return nullptr;
+  }
+  for (Py_ssize_t i = 0; i < n; ++i)
+    if (!PyType_Check(v[i])) {
+      PyErr_SetString(PyExc_TypeError, "problem_classes takes classes");
+      return nullptr;
+    }
+  take_class<mega_moe_norm_problem>(v[0]);
+  take_class<mega_moe_gate_problem>(v[1]);
+  take_class<mega_moe_topk_problem>(v[2]);
+  take_class<mega_moe_sort_problem>(v[3]);
+  take_class<mega_moe_unsort_problem>(v[4]);
+  take_class<mega_moe_product_problem>(v[5]);
+  take_class<mega_moe_act_problem>(v[6]);
+  Py_RETURN_NONE;
 }
 
 void* stream_of(PyObject* o, at::Device dev) {
@@ -311,6 +346,7 @@ PyObject* act_backward(PyObject*, PyObject* const* v, Py_ssize_t n) {
 }
 
 PyMethodDef methods[] = {
+    {"problem_classes", (PyCFunction)(void (*)(void))problem_classes, METH_FASTCALL, nullptr},
     {"norm_quant", (PyCFunction)(void (*)(void))norm_quant, METH_FASTCALL, nullptr},
     {"gate_logits", (PyCFunction)(void (*)(void))gate_logits, METH_FASTCALL, nullptr},
     {"gate_topk", (PyCFunction)(void (*)(void))gate_topk, METH_FASTCALL, nullptr},
