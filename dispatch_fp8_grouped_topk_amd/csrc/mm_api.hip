@@ -13,6 +13,7 @@
 #include "mm_common.h"
 #include "mm_front.h"
 #include "mm_parts.h"
+#include "mm_product_policy.h"
 
 #define MM_EXPORT extern "C" __attribute__((visibility("default")))
 
@@ -803,7 +804,8 @@ MM_EXPORT int mega_moe_block_product(const mega_moe_product_problem* p, const vo
   if (!p) return MEGA_MOE_ERR_NULL_POINTER;
   if (p->num_rows < 0 || p->num_rows >= kMaxTokens || p->n <= 0 || p->n % 8 || p->n > mm::kMaxProductN || bad_hidden(p->k) ||
       p->num_groups < 1 || p->num_groups > mm::kMaxExperts || p->flags || bad_stride(p->x_stride, p->k, 16) ||
-      p->x_stride > mm::kMaxProductStride || bad_stride(p->y_stride, p->n, 8))
+      p->x_stride > mm::kMaxProductStride || bad_stride(p->y_stride, p->n, 8) ||
+      p->num_rows * p->n >= mm::kMaxProductArea)
     return MEGA_MOE_ERR_INVALID_ARG;
   const int64_t M = p->num_rows, N = p->n, K = p->k, G = p->num_groups;
   if (M == 0) return MEGA_MOE_OK;

@@ -19,6 +19,11 @@ __device__ __forceinline__ v4f mfma_block(const v8i& a, const v8i& b) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, z, 0, 0, 0, 0, 0, 0);
 }
 
+// A launch's part of the items: slabs of weight rows times tiles of rows, `count` of them from `first`.
+struct ProductPart {
+  int slabs, tiles, first, count;
+};
+
 // The rows of group g, whatever the offsets hold.
 __device__ __forceinline__ void group_rows(const ProductArgs& a, int g, int& lo, int& hi) {
   lo = 0;
@@ -118,7 +123,7 @@ struct LargeLds {
 };
 
 template <int kNG, int kWN, int kKS, int kStages>
-__global__ __launch_bounds__(512) void k_product_large(ProductArgs a, int slabs, int tiles) {
+__global__ __launch_bounds__(512) void k_product_large(ProductArgs a, ProductPart part) {
   using L = LargeLds<kNG, kWN, kKS, kStages>;
   constexpr int kBN = L::kBN, kBM = L::kBM, kWM = L::kWM, kGW = 8 / kKS;     // kGW: waves that share a block
   constexpr int kWLoads = kBN / 8 / kGW, kXLoads = (kBM / 8 + kGW - 1) / kGW, kSLoads = (kBM / 16 + kGW - 1) / kGW,
@@ -131,9 +136,9 @@ __global__ __launch_bounds__(512) void k_product_large(ProductArgs a, int slabs,
   const int w8 = __builtin_amdgcn_readfirstlane(tid >> 6), ks = w8 / kGW, w = w8 % kGW, wm = w % kWN, wn = w / kWN;
   const int KB = a.K / 128, steps = (KB + kKS - 1) / kKS;
   // each XCD walks a contiguous range of items; an item is (band of 4 tiles, slab, tile of the band)
-  const int per_xcd = gridDim.x >> 3, item = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
-  if (item >= slabs * tiles) return;
-  const int band = item / (4 * slabs), in = item - band * 4 * slabs, high = min(4, tiles - 4 * band);
+  const int at = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3), item = part.first + at;
+  if (at >= part.count) return;
+  const int slabs = part.slabs, band = item / (4 * slabs), in = item - band * 4 * slabs, high = min(4, part.tiles - 4 * band);
   const int slab = in / high, t = 4 * band + in - slab * high;
   const Tile tile = find_tile<kBM, 512>(a, t, lds.sh, &lds.tile);
   if (tile.rows <= 0) return;
@@ -344,15 +349,15 @@ struct SplitLds {
 };
 
 template <int kRT, int kCT, int kWaves, int kStages, int kBlocks>
-__global__ __launch_bounds__(64 * kWaves) void k_product_split(ProductArgs a, int slabs, int tiles) {
+__global__ __launch_bounds__(64 * kWaves) void k_product_split(ProductArgs a, ProductPart part) {
   using L = SplitLds<kRT, kCT, kWaves, kStages, kBlocks>;
   constexpr int kLoads = 2 * (kRT + kCT);
   __shared__ __align__(1024) L lds;
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), lr = lane & 15, lg = lane >> 4;
   const int KB = a.K / 128;
-  const int per_xcd = gridDim.x >> 3, item = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
-  if (item >= slabs * tiles) return;
-  const int slab = item / tiles, t = item - slab * tiles;
+  const int at = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3), item = part.first + at;
+  if (at >= part.count) return;
+  const int slab = item / part.tiles, t = item - slab * part.tiles;
   const Tile tile = find_tile<16 * kCT, 64 * kWaves>(a, t, lds.sh, &lds.tile);
   if (tile.rows <= 0) return;
   const int g = __builtin_amdgcn_readfirstlane(tile.g), m0 = __builtin_amdgcn_readfirstlane(tile.m0),
@@ -464,15 +469,18 @@ __global__ __launch_bounds__(64 * kWaves) void k_product_split(ProductArgs a, in
   }
 }
 
-// One launch of kTile workgroups for every slab of weight rows and every tile that the groups may be cut into.
+// A workgroup for every slab of weight rows and every tile that the groups may be cut into.
 template <int kVariant, class F>
 hipError_t launch(const ProductArgs& a, hipStream_t s, int threads, F* kernel) {
   constexpr ProductTile t = kProductTiles[kVariant];
-  const int slabs = (a.N + t.n - 1) / t.n, whole = (a.M + t.m - 1) / t.m;
-  const int tiles = a.offset ? std::min(a.M, whole + a.G) : whole;
-  if ((int64_t)slabs * tiles > 2 * kProductGroups) return hipErrorInvalidValue;   // no buffers are that large
-  hipLaunchKernelGGL(kernel, dim3((unsigned)((slabs * tiles + 7) / 8 * 8)), dim3(threads), 0, s, a, slabs, tiles);
-  return hipGetLastError();
+  const int64_t items = product_items(t, a.M, a.N, a.G, a.offset != nullptr);
+  for (int64_t first = 0; first < items; first += kProductGroups) {
+    const int count = (int)std::min(items - first, kProductGroups);
+    const ProductPart part{(int)up_div(a.N, t.n), (int)product_tiles(t, a.M, a.G, a.offset != nullptr), (int)first, count};
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(count + 7) / 8 * 8), dim3(threads), 0, s, a, part);
+    if (const hipError_t e = hipGetLastError()) return e;
+  }
+  return hipSuccess;
 }
 
 template <int kVariant, int kWaves, int kStages>

@@ -25,11 +25,24 @@ constexpr ProductTile kProductTiles[] = {
     {256, 64, 2.5f, .518f, 128}, {256, 128, 3.3f, .724f, 128}, {256, 256, 3.9f, 1.27f, 128}};
 constexpr int kProductCount = sizeof(kProductTiles) / sizeof(kProductTiles[0]), kProductSplit = 5;
 
-// Most workgroups of a launch, whose threads are counted in 32 bits; the largest tile never has more (y alone would pass
-// 2^39 bytes, or there are at most 2^22 of its tiles).
+// Most workgroups of a launch, whose threads are counted in 32 bits (512 each).  More are launched in parts; only the largest
+// tile can need that (4096 rows by 1024 groups of 2^20 x 128 weights), the others are passed over then.
 constexpr int64_t kProductGroups = 1 << 22;
 
+// Least num_rows * n that is refused: below it a launch's items (product_items) fit 31 bits.
+constexpr int64_t kMaxProductArea = (int64_t)1 << 45;
+
 constexpr int64_t up_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Items of a launch, a workgroup each: every slab of weight rows and every tile that the groups may be cut into, with rows or
+// without.
+constexpr int64_t product_tiles(const ProductTile& t, int64_t M, int64_t G, bool by_group) {
+  const int64_t whole = up_div(M, t.m);
+  return !by_group ? whole : M < whole + G ? M : whole + G;
+}
+constexpr int64_t product_items(const ProductTile& t, int64_t M, int64_t N, int64_t G, bool by_group) {
+  return up_div(N, t.n) * product_tiles(t, M, G, by_group);
+}
 
 // Workgroups that have rows: the rows of G groups are not known here and taken as uneven, each group's last tile as
 // about half full.

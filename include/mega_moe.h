@@ -513,7 +513,7 @@ int mega_moe_unsort_backward(const mega_moe_unsort_problem* p, const void* dy, c
                              const int32_t* pair_pos, const float* topk_w, void* d_rows, float* d_w, void* stream);
 
 typedef struct {
-  int64_t num_rows;      /* M in [0, 2^30) */
+  int64_t num_rows;      /* M in [0, 2^30), M * N below 2^45 */
   int32_t n;             /* N in (0, 2^20], multiple of 8: rows of each group's weights */
   int32_t k;             /* K in (0, 16384], multiple of 128 */
   int32_t num_groups;    /* G in [1, 8192] */
