@@ -24,16 +24,6 @@ struct ProductPart {
   int slabs, tiles, first, count;
 };
 
-// The rows of group g, whatever the offsets hold.
-__device__ __forceinline__ void group_rows(const ProductArgs& a, int g, int& lo, int& hi) {
-  lo = 0;
-  hi = a.M;
-  if (a.offset) {
-    lo = min(max(a.offset[g], 0), a.M);
-    hi = min(max(a.offset[g + 1], lo), a.M);
-  }
-}
-
 // ------------------------------------------------------------------------------- many rows
 // A workgroup takes 64 kWN weight rows x 16 kNG kWM rows of x, its eight waves (two a SIMD) 64 weight rows (wm = wave % kWN)
 // and kNG groups of 16 rows of x (kWM i + wave / kWN) each.  With kKS 2 the waves are two sets of four that take every other
@@ -77,37 +67,17 @@ __device__ __forceinline__ v8i lds_operand(const uint8_t* lo, const uint8_t* hi,
 }
 
 // Tile `t` of the tiles of at most kBM rows that the groups are cut into: its group, first row and rows (0: there is none).
-struct Tile {
-  int g, m0, rows;
-};
 template <int kBM, int kThreads>
-__device__ __forceinline__ Tile find_tile(const ProductArgs& a, int t, int* sh, Tile* found) {
+__device__ __forceinline__ Tile find_tile(const ProductArgs& a, int t, int tiles, uint32_t* sh, Tile* found) {
   if (!a.offset) return Tile{0, t * kBM, min(kBM, a.M - t * kBM)};
   const int tid = threadIdx.x, per = (a.G + kThreads - 1) / kThreads;
   const int g0 = min(tid * per, a.G), g1 = min(g0 + per, a.G);
   if (tid == 0) *found = Tile{0, 0, 0};
-  int sum = 0;
-  for (int g = g0; g < g1; ++g) {
-    int lo, hi;
-    group_rows(a, g, lo, hi);
-    sum += (hi - lo + kBM - 1) / kBM;
-  }
-  int v[1] = {sum}, all[1];
+  const uint32_t sum = tiles_of(a.offset, g0, g1, a.M, kBM, tiles);
+  uint32_t v[1] = {sum}, all[1];
   block_scan_n<1, kThreads>(v, sh, all);
-  int before = v[0] - sum;
-  if (t >= before && t < v[0]) {
-    for (int g = g0; g < g1; ++g) {
-      int lo, hi;
-      group_rows(a, g, lo, hi);
-      const int n = (hi - lo + kBM - 1) / kBM;
-      if (t < before + n) {
-        const int m0 = lo + (t - before) * kBM;
-        *found = Tile{g, m0, min(kBM, hi - m0)};
-        break;
-      }
-      before += n;
-    }
-  }
+  const uint32_t before = v[0] - sum;
+  if ((uint32_t)t >= before && (uint32_t)t < v[0]) *found = tile_among(a.offset, g0, g1, a.M, kBM, (uint32_t)t - before);
   __syncthreads();
   return *found;
 }
@@ -118,7 +88,7 @@ struct LargeLds {
   static constexpr int kW = kBN * 128, kX = kBM * 128, kBlock = kW + kX + kBM * 16, kStage = kKS * kBlock;
   uint8_t ring[kStages * kStage];
   float wsc[(kBN + 127) / 128][kMaxKBlocks];
-  int sh[32];
+  uint32_t sh[32];
   Tile tile;
 };
 
@@ -140,7 +110,7 @@ __global__ __launch_bounds__(512) void k_product_large(ProductArgs a, ProductPar
   if (at >= part.count) return;
   const int slabs = part.slabs, band = item / (4 * slabs), in = item - band * 4 * slabs, high = min(4, part.tiles - 4 * band);
   const int slab = in / high, t = 4 * band + in - slab * high;
-  const Tile tile = find_tile<kBM, 512>(a, t, lds.sh, &lds.tile);
+  const Tile tile = find_tile<kBM, 512>(a, t, part.tiles, lds.sh, &lds.tile);
   if (tile.rows <= 0) return;
   const int g = __builtin_amdgcn_readfirstlane(tile.g), m0 = __builtin_amdgcn_readfirstlane(tile.m0),
             rows = __builtin_amdgcn_readfirstlane(tile.rows), n0 = slab * kBN, nrows = min(kBN, a.N - n0);
@@ -344,7 +314,7 @@ struct SplitLds {
   static constexpr int kSums = kWaves * kRT * kCT * 1024, kMain = kWaves * kRing > kSums ? kWaves * kRing : kSums;
   uint8_t main[kMain];                           // the waves' rings, then their sums
   float sw[kMaxKBlocks], sx[16 * kCT * (kBlocks | 1)];   // the weights' scales [KB], the rows' [16 kCT][KB | 1]
-  int sh[32];
+  uint32_t sh[32];
   Tile tile;
 };
 
@@ -358,7 +328,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_product_split(ProductArgs a, Pr
   const int at = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3), item = part.first + at;
   if (at >= part.count) return;
   const int slab = item / part.tiles, t = item - slab * part.tiles;
-  const Tile tile = find_tile<16 * kCT, 64 * kWaves>(a, t, lds.sh, &lds.tile);
+  const Tile tile = find_tile<16 * kCT, 64 * kWaves>(a, t, part.tiles, lds.sh, &lds.tile);
   if (tile.rows <= 0) return;
   const int g = __builtin_amdgcn_readfirstlane(tile.g), m0 = __builtin_amdgcn_readfirstlane(tile.m0),
             rows = __builtin_amdgcn_readfirstlane(tile.rows), n0 = slab * 16 * kRT, nrows = min(16 * kRT, a.N - n0);

@@ -44,6 +44,43 @@ constexpr int64_t product_items(const ProductTile& t, int64_t M, int64_t N, int6
   return up_div(N, t.n) * product_tiles(t, M, G, by_group);
 }
 
+// The rows of group g among M, whatever the offsets hold (NULL: all of them).
+struct GroupRows {
+  int lo, hi;
+};
+constexpr GroupRows group_rows(const int32_t* offset, int g, int M) {
+  if (!offset) return GroupRows{0, M};
+  const int from = offset[g] < 0 ? 0 : offset[g], lo = from < M ? from : M;
+  const int to = offset[g + 1] < lo ? lo : offset[g + 1];
+  return GroupRows{lo, to < M ? to : M};
+}
+// The tiles of m rows of groups [g0, g1), `tiles` at most: a launch has no more, and groups whose offsets ascend have no
+// more.  Where they descend the true number may pass 32 bits; 512 times this one does not, so each tile has one finder.
+constexpr uint32_t tiles_of(const int32_t* offset, int g0, int g1, int M, int m, int tiles) {
+  uint32_t sum = 0;
+  for (int g = g0; g < g1; ++g) {
+    const GroupRows r = group_rows(offset, g, M);
+    sum += (uint32_t)(r.hi - r.lo + m - 1) / (uint32_t)m;
+  }
+  return sum < (uint32_t)tiles ? sum : (uint32_t)tiles;
+}
+// The group and rows of the k-th of those tiles.
+struct Tile {
+  int g, m0, rows;
+};
+constexpr Tile tile_among(const int32_t* offset, int g0, int g1, int M, int m, uint32_t k) {
+  for (int g = g0; g < g1; ++g) {
+    const GroupRows r = group_rows(offset, g, M);
+    const uint32_t n = (uint32_t)(r.hi - r.lo + m - 1) / (uint32_t)m;
+    if (k < n) {
+      const int m0 = r.lo + (int)k * m;
+      return Tile{g, m0, r.hi - m0 < m ? r.hi - m0 : m};
+    }
+    k -= n;
+  }
+  return Tile{0, 0, 0};
+}
+
 // Workgroups that have rows: the rows of G groups are not known here and taken as uneven, each group's last tile as
 // about half full.
 constexpr int64_t product_workgroups(const ProductTile& t, int64_t M, int64_t N, int64_t G) {

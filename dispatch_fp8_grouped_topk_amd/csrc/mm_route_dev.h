@@ -55,10 +55,10 @@ __device__ __forceinline__ void route_count_block(const Args& a, int b, int* his
   __syncthreads();
 }
 
-// Inclusive scans of N ints per thread at once over an NT-thread workgroup (one round of
+// Inclusive scans of N ints (T: with a sign or without) per thread at once over an NT-thread workgroup (one round of
 // barriers for all N); totals of each written to total[0..N).  sh must hold 32 * N ints.
-template <int N, int NT>
-__device__ __forceinline__ void block_scan_n(int v[N], int* sh, int total[N]) {
+template <int N, int NT, class T>
+__device__ __forceinline__ void block_scan_n(T v[N], T* sh, T total[N]) {
   static_assert(NT % 64 == 0 && NT <= 1024, "up to 16 waves");
   constexpr int NW = NT / 64;
   const int tid = threadIdx.x;
@@ -67,7 +67,7 @@ __device__ __forceinline__ void block_scan_n(int v[N], int* sh, int total[N]) {
   for (int d = 1; d < 64; d <<= 1) {
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      const int o = __shfl_up(v[n], d, 64);
+      const T o = __shfl_up(v[n], d, 64);
       if (lane >= d) v[n] += o;
     }
   }
@@ -78,9 +78,9 @@ __device__ __forceinline__ void block_scan_n(int v[N], int* sh, int total[N]) {
   if (w == 0) {
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      int x = lane < NW ? sh[n * 32 + lane] : 0;
+      T x = lane < NW ? sh[n * 32 + lane] : 0;
       for (int d = 1; d < 16; d <<= 1) {
-        const int o = __shfl_up(x, d, 64);
+        const T o = __shfl_up(x, d, 64);
         if (lane >= d) x += o;
       }
       if (lane < 16) sh[n * 32 + 16 + lane] = x;
