@@ -33,13 +33,14 @@ struct ProductPart {
 // ring in LDS by loads that need no registers; a block's MFMAs run while the next ones are on their way.  16-byte chunk c of
 // a row r sits at c ^ (r / 2 % 8), so that the 16 rows of an operand read fall into different banks.
 //
-// 8192 x 4096 x 7168 in tiles of 256 x 256 takes 217 to 231 us by box, 2080 to 2215 TFLOP/s, of the 159 us at the 3025 TFLOP/s that a large library
-// product with one scale a tensor reaches here.  The matrix units are busy 47% of the cycles at the 2.1 GHz of the loaded chip;
-// a block takes about 4000 cycles for 2048 of MFMAs: the scaling (four multiply-adds an MFMA) runs beside the MFMAs in a
-// register-only loop (4% longer than without), LDS is busy a quarter of the time, and with every workgroup on the same tile,
-// so that all lines come from the L2, it still takes 204 us; what is left is waiting for a ring of two blocks.  Three blocks
-// of 256 x 256 do not fit into LDS; 256 x 128 with three takes 241.  32x32x64 MFMAs save nothing (256 x 128: 255 us against
-// 246) and spill at 256 x 256.  Loads in one burst behind the first group's MFMAs: 230; band heights 2 and 8 instead of 4: 232, 226.
+// 8192 x 4096 x 7168 in tiles of 256 x 256 takes 218 to 231 us by box, 2080 to 2210 TFLOP/s, of the 160 us at the 3000 TFLOP/s
+// that a large library product with one scale a tensor reaches here.  The matrix units are busy half of the cycles (2.1 GHz on
+// the loaded chip): a block takes about 4100 for 2048 of MFMAs.  The scaling (four multiply-adds an MFMA) runs beside the MFMAs
+// in a register-only loop (4% longer than without), LDS is busy a quarter of the time, and with every workgroup on the same
+// tile, so that all lines come from the L2, it still takes 204 us; the loop without barriers or without loads has not been
+// timed, so the rest is not explained.  (Times of a change, here and below, are of one box each.)  Three blocks of 256 x 256 do
+// not fit into LDS; 256 x 128 with three takes 241.  32x32x64 MFMAs save nothing (256 x 128: 255 us against 246) and spill at
+// 256 x 256.  Loads in one burst behind the first group's MFMAs: 230; band heights 2 and 8 instead of 4: 232, 226.
 typedef __amdgpu_buffer_rsrc_t rsrc_t;
 __device__ __forceinline__ rsrc_t make_rsrc(const void* base, size_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)(uint32_t)bytes, 0x00020000);

@@ -1,7 +1,7 @@
 // Tokens sorted by expert and back: the plan (places of the pairs), the rows' way there, and the weighted way back with
 // its gradient.  Everything moves rows of some kilobytes as 16-byte pieces, so the memory system is the bound; the plan
 // is integers that depend on positions alone, never on the order in which atomics return.  A large copy reaches 5.1 TB/s
-// here, writing alone 6.8.
+// here, reading alone 7.2, writing alone 6.9.
 //
 //   place of pair p with expert e:  #{pairs of experts below e} + #{pairs p' < p of e}
 //   y[t] = sum_j w[t, j] rows[place(t, j)];  d_rows[place] = w dy[t];  d_w[t, j] = <rows[place], dy[t]>
@@ -17,7 +17,7 @@ namespace {
 // counting the pairs that sort before each: with key(p) = expert * 4096 + p they are those with a smaller key.  A
 // comparison of 64 pairs is one vector instruction and a count of bits, so 4096 pairs take 16 of them a wave and pair;
 // that is cheaper than the other launches (E 256, k 8, 8-bit rows of 7168 columns: 511 tokens 13.0 us, 513 in blocks 14.9).
-// The last workgroup makes expert_offset.  One token takes 4.5 us on the card: the launch, one memory latency for the ids and
+// The last workgroup makes expert_offset.  One token takes 4.4 us on the card: the launch, one memory latency for the ids and
 // the row, two barriers, the stores.
 template <bool kMove, int kIds>
 __global__ __launch_bounds__(256) void k_sort_small(SortArgs a, int parts) {
@@ -189,9 +189,10 @@ __global__ __launch_bounds__(1024) void k_sort_bases(SortArgs a) {
 
 // 3. Places and rows: a wave takes a token, reads its row once and writes it k times, past the caches.  Every workgroup makes
 // the experts' offsets from their totals itself (a kilobyte at 256 experts) rather than in a launch of their own.
-// T 8192, H 7168, E 256, k 8 in BF16 (1.02 GB, a floor of 201 us at the rate of a large copy) takes 216 us with the two
-// kernels before (10): bound by writing.  Stores through the caches took 328; the other way round, a wave a place that reads its
-// token's row from the caches, 257 with stores past them and 310 to 575 through them.
+// T 8192, H 7168, E 256, k 8 in BF16 (0.12 GB read, 0.91 written: 201 us at the rate of a large copy, 147 at those of reading
+// and of writing alone) takes 208 us, and 9 for the two kernels before: bound by writing.  In all, stores through the caches
+// took 328; the other way round, a wave a place that reads its token's row from the caches, 257 with stores past them and 310
+// to 575 through them.
 template <bool kMove>
 __global__ __launch_bounds__(256) void k_sort_move(SortArgs a) {
   extern __shared__ int s_off[];                 // [E]
@@ -298,7 +299,7 @@ namespace {
 // ---------------------------------------------------------------------------------------- back
 // A thread takes eight columns of a token: k places, then k pieces of rows under way at once, eight at a time, added up in
 // ascending order.  T 4091, H 4096, k 8 in float32 (550 MB) takes 100 us, 5.5 TB/s (stores through the caches: 106), a decode
-// batch of 128 x 7168 4.2 us on the card: two memory latencies after the launch.
+// batch of 128 x 7168 4.8 to 5.0 us on the card: two memory latencies after the launch.
 template <bool kF32>
 __global__ __launch_bounds__(256) void k_unsort(UnsortArgs a) {
   const int cpt = a.H / 8;
@@ -339,8 +340,8 @@ __global__ __launch_bounds__(256) void k_unsort(UnsortArgs a) {
 // A workgroup takes a token, or for few tokens (kSplit) four of its pairs, its threads eight columns each (two times eight
 // beyond 8192 columns): dy stays in registers,
 // each pair's row is read once for d_w and written once.  Sums of eight products are float32, the rest of d_w's sum is
-// float64: lanes by DPP, waves through LDS in a fixed order.  T 8192, H 7168, k 8 in BF16 (2.0 GB) takes 397 us, 5.0 TB/s;
-// T 1021, H 4096 21.6 us, 6.0 TB/s (stores through the caches: 29.7).
+// float64: lanes by DPP, waves through LDS in a fixed order.  T 8192, H 7168, k 8 in BF16 (2.0 GB) takes 395 us, 5.1 TB/s;
+// T 1021, H 4096 21.5 us, 6.0 TB/s (stores through the caches: 29.7).
 constexpr int kAtOnce = 4;                       // pairs whose rows are under way at once
 template <bool kF32, int kNC, bool kSplit>
 __global__ __launch_bounds__(1024) void k_unsort_backward(UnsortArgs a) {
